@@ -387,6 +387,55 @@ quip_status quip_qmatvec(const quip_transform* tf, const uint32_t* packed, int64
                          const float* scale, int bits, const void* x, int x_dtype, int64_t ldx, int64_t B,
                          float* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 
+/* The largest number of alternatives quip_logprobs returns per row. */
+#define QUIP_LOGPROBS_MAX_TOP 32
+
+/*
+ * What a (quantized) output layer's logits say of given tokens: for each of
+ * T rows x of V logits,
+ *   lse     = ln sum_v exp(x_v),        p_v = exp(x_v - lse)
+ *   logprob = x_tok - lse               (0 where the row's token is -1: none given)
+ *   entropy = -sum_v p_v ln p_v         (a term with p_v = 0 counts 0)
+ *   top_values[0..k), top_ids[0..k)     the k largest x_v - lse with their v, largest
+ *                                       first, equal logits by increasing v
+ * in one pass over the logits; sums in fp32.  Perplexity (QuIP, Experiments,
+ * the language-generation evaluations) is exp(-mean logprob).
+ *   logits : device T x V, QUIP_F32 or QUIP_BF16, row stride ld >= V; any
+ *            alignment (16-byte loads start at each row's first boundary).
+ *   tokens : device T int32 in [-1, V); anything else sets QUIP_ERR_ARG in
+ *            the status word and counts as -1.  NULL together with logprob.
+ *   logprob, entropy, lse : device T fp32; entropy and lse may be NULL.
+ *   k      : 0 .. min(V, QUIP_LOGPROBS_MAX_TOP); top_values (fp32) and top_ids
+ *            (int32): device T x k, ignored when k is 0.
+ * A logit of -inf has probability 0.  A row of nothing else has lse,
+ * logprob and top_values -inf and entropy 0.  A NaN or +inf makes the row's
+ * values NaN (its top_ids are then unspecified, in [0, V)).
+ * T <= 2^22, V <= 2^28; T = 0 does nothing.
+ */
+quip_status quip_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int32_t* tokens,
+                          float* logprob, float* entropy, float* lse, int k, float* top_values, int32_t* top_ids,
+                          void* stream);
+
+/*
+ * The gradient of quip_logprobs' logprob and entropy with respect to the
+ * logits:
+ *   d_logits[v] = g_logprob (1[v = tok] - p_v) - g_entropy p_v (ln p_v + entropy),
+ * p_v = exp(x_v - lse); a row's token of -1 counts as g_logprob = 0.
+ *   lse, entropy : device T fp32, as quip_logprobs wrote them (entropy is
+ *                  needed with g_entropy only).
+ *   g_logprob, g_entropy : device T fp32, the gradients of the row's logprob
+ *                  and entropy; NULL counts as 0.  tokens is needed with
+ *                  g_logprob.
+ *   d_logits : device T x V of the logits' type, row stride ldd >= V; may be
+ *                  the logits themselves (ldd == ld), else must not overlap them.
+ * Rows whose two gradients are 0 (padding), and rows of -inf only, are set
+ * to 0 whatever their logits hold.  Other errors and sizes as quip_logprobs.
+ */
+quip_status quip_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                   const int32_t* tokens, const float* lse, const float* entropy,
+                                   const float* g_logprob, const float* g_entropy, void* d_logits, int64_t ldd,
+                                   void* stream);
+
 /* W_hat_t[i,j] = lo[i] + scale[i] * codes[i,j]  (device; m x n, row stride n). */
 quip_status quip_dequantize(const uint8_t* codes, const float* lo, const float* scale,
                             int64_t m, int64_t n, float* W_hat_t, void* stream);

@@ -74,7 +74,7 @@ __all__ = [
     "run_pipeline", "STREAM_M_SIGNS", "STREAM_N_SIGNS", "STREAM_M_A", "STREAM_M_B",
     "STREAM_N_A", "STREAM_N_B", "STREAM_M_PERM", "STREAM_N_PERM", "random_permutation",
     "diag_order", "greedy_pass", "quantize_layer", "code_slot_bits", "packed_words", "pack_codes",
-    "unpack_codes", "quantized_matvec",
+    "unpack_codes", "quantized_matvec", "token_logprobs", "token_logprobs_grad",
 ]
 
 # ----------------------------------------------------------------------------
@@ -603,6 +603,57 @@ def quantized_matvec(codes: np.ndarray, lo: np.ndarray, s: np.ndarray, U: SideTr
     original-domain matrix times each vector."""
     W_hat = incoherence_inverse(dequantize(codes, lo, s), U, V)
     return np.asarray(x, dtype=np.float64) @ W_hat.T
+
+
+# ----------------------------------------------------------------------------
+# Scoring tokens by an output layer's logits
+# ----------------------------------------------------------------------------
+
+
+def token_logprobs(x: np.ndarray, tokens: np.ndarray, k: int = 0):
+    """(logprob, entropy, lse, top_values, top_ids) of the rows of logits x
+    (T, V): ln softmax at the given token (0 for token -1), entropy, log of
+    the sum of exponentials, and the k largest log probabilities, equal
+    logits by increasing index.  A row of -inf only has lse, logprob and
+    values of -inf and entropy 0."""
+    x = np.asarray(x, dtype=np.float64)
+    T, V = x.shape
+    logprob, entropy, lse = np.zeros(T), np.zeros(T), np.zeros(T)
+    values, ids = np.zeros((T, k)), np.zeros((T, k), dtype=np.int64)
+    for t in range(T):
+        top = np.max(x[t])
+        if top == -np.inf:
+            lse[t], p = -np.inf, np.zeros(V)
+            logp = np.full(V, -np.inf)
+        else:
+            lse[t] = top + np.log(np.sum(np.exp(x[t] - top)))
+            logp = x[t] - lse[t]
+            p = np.exp(logp)
+        entropy[t] = -np.sum(p[p > 0] * logp[p > 0])
+        if tokens[t] >= 0:
+            logprob[t] = logp[tokens[t]]
+        ids[t] = np.lexsort((np.arange(V), -x[t]))[:k]
+        values[t] = logp[ids[t]]
+    return logprob, entropy, lse, values, ids
+
+
+def token_logprobs_grad(x: np.ndarray, tokens: np.ndarray, lse: np.ndarray, entropy: np.ndarray,
+                        g_logprob: np.ndarray, g_entropy: np.ndarray) -> np.ndarray:
+    """d/dx of sum_t g_logprob[t] logprob[t] + g_entropy[t] entropy[t]:
+    g (1[v = tok] - p_v) - ge p_v (ln p_v + entropy), g = 0 without a token."""
+    x = np.asarray(x, dtype=np.float64)
+    d = np.zeros_like(x)
+    for t in range(x.shape[0]):
+        if lse[t] == -np.inf:
+            continue
+        logp = x[t] - lse[t]
+        p = np.exp(logp)
+        live = p > 0
+        g = g_logprob[t] if tokens[t] >= 0 else 0.0
+        d[t, live] = -p[live] * (g + g_entropy[t] * (logp[live] + entropy[t]))
+        if tokens[t] >= 0:
+            d[t, tokens[t]] += g
+    return d
 
 
 # ----------------------------------------------------------------------------

@@ -24,6 +24,7 @@ __all__ = [
     "quip_incoherence_inverse", "quip_ldl", "quip_ldlq_quantize", "quip_dequantize",
     "quip_nearest_quantize", "quip_diag_order", "quip_permute", "quip_greedy_refine", "METHODS",
     "quip_packed_words", "quip_pack_codes", "quip_qmatvec", "QuantizedLinear",
+    "quip_logprobs", "quip_logprobs_backward", "TokenScores",
     "quip_workspace_size", "quip_layer_workspace_size", "quip_quantize_layer", "quip_quantize_layer_host",
     "layer_views", "quip_sync_status", "quip_timing_begin", "quip_timing_end", "quip_timing_trace", "LayerQuantizer",
     "LayerGroupQuantizer", "quantize_layer", "QuipError",
@@ -64,6 +65,37 @@ def _cuda(t: torch.Tensor, name: str) -> None:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
 
+
+def _here(name: str, t: torch.Tensor, dtypes, shape, device=None, rows: bool = False) -> int:
+    """The address of t, once it is a tensor of one of ``dtypes`` and of
+    ``shape`` (None: any size) on the current device, with contiguous rows
+    (``rows``: any row stride) or contiguous altogether."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != (torch.cuda.current_device() if device is None else device):
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != s for s, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"{tuple('any' if w is None else w for w in shape)}")
+    if rows:
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+            raise ValueError(f"{name} has overlapping rows")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride of a 2-D tensor; one row has whatever stride its columns need."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+_F32, _I32 = (torch.float32,), (torch.int32,)
+_FLOATS = (torch.float32, torch.bfloat16)
 
 _cudart = None
 
@@ -346,6 +378,88 @@ class QuantizedLinear:
             out = torch.empty(x.shape[0], self.m, dtype=torch.float32, device=x.device)
         quip_qmatvec(self.tf, self.packed, self.lo, self.scale, self.bits, x, out, self.ws, self.stream)
         return out
+
+    def score(self, x: torch.Tensor, tokens: torch.Tensor, top: int = 0) -> "TokenScores":
+        """The layer as a model's output layer: the log probabilities of
+        ``tokens`` (T int32, -1: none) under the softmax of W^ x[t], with entropy
+        and the ``top`` best alternatives.  T may exceed max_batch: the logits
+        exist max_batch rows at a time.  exp(-logprob.mean()) is the perplexity."""
+        T, dev = x.shape[0], x.device
+        if tokens.shape != (T,):
+            raise ValueError(f"tokens has shape {tuple(tokens.shape)}, expected ({T},)")
+        if not 0 <= top <= min(self.m, L.QUIP_LOGPROBS_MAX_TOP):
+            raise ValueError(f"top={top}")
+        with torch.cuda.stream(self.stream if self.stream is not None else torch.cuda.current_stream()):
+            r = TokenScores(*(torch.empty(T, dtype=torch.float32, device=dev) for _ in range(3)))
+            if top:
+                r.top_values = torch.empty(T, top, dtype=torch.float32, device=dev)
+                r.top_ids = torch.empty(T, top, dtype=torch.int32, device=dev)
+            logits = torch.empty(min(T, self.max_batch), self.m, dtype=torch.float32, device=dev)
+            for a in range(0, T, self.max_batch):
+                b = min(T, a + self.max_batch)
+                y = self(x[a:b], logits[:b - a])
+                quip_logprobs(y, tokens[a:b], r.logprob[a:b], r.entropy[a:b], r.lse[a:b],
+                              r.top_values[a:b] if top else None, r.top_ids[a:b] if top else None, self.stream)
+        return r
+
+
+def quip_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], logprob: Optional[torch.Tensor],
+                  entropy: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                  top_values: Optional[torch.Tensor] = None, top_ids: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """logprob[t] = ln p(tokens[t]) under the softmax of logits[t] (0 where
+    tokens[t] is -1), the row's entropy and log-sum-exp, and its k largest log
+    probabilities with their indices (top_values, top_ids: T x k), in one pass
+    (include/quip.h)."""
+    T, V = logits.shape
+    dev = torch.cuda.current_device() if logits.is_cuda else None
+    x = _here("logits", logits, _FLOATS, (T, V), dev, rows=True)
+    if (tokens is None) != (logprob is None):
+        raise ValueError("tokens and logprob go together")
+    if (top_values is None) != (top_ids is None):
+        raise ValueError("top_values and top_ids go together")
+    k = 0 if top_ids is None else top_ids.shape[1]
+    L.check(load().quip_logprobs(
+        x, _dtype(logits), T, V, _row_stride(logits),
+        None if tokens is None else _here("tokens", tokens, _I32, (T,), dev),
+        None if logprob is None else _here("logprob", logprob, _F32, (T,), dev),
+        None if entropy is None else _here("entropy", entropy, _F32, (T,), dev),
+        None if lse is None else _here("lse", lse, _F32, (T,), dev), k,
+        None if k == 0 else _here("top_values", top_values, _F32, (T, k), dev),
+        None if k == 0 else _here("top_ids", top_ids, _I32, (T, k), dev), _s(stream)), "quip_logprobs")
+
+
+def quip_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor], lse: torch.Tensor,
+                           d_logits: torch.Tensor, g_logprob: Optional[torch.Tensor] = None,
+                           g_entropy: Optional[torch.Tensor] = None, entropy: Optional[torch.Tensor] = None,
+                           stream=None) -> None:
+    """d_logits = the gradient of sum_t g_logprob[t] logprob[t] + g_entropy[t]
+    entropy[t] with respect to the logits; d_logits may be the logits."""
+    T, V = logits.shape
+    dev = torch.cuda.current_device() if logits.is_cuda else None
+    x = _here("logits", logits, _FLOATS, (T, V), dev, rows=True)
+    d = _here("d_logits", d_logits, (logits.dtype,), (T, V), dev, rows=True)
+    if g_logprob is not None and tokens is None:
+        raise ValueError("g_logprob needs tokens")
+    if g_entropy is not None and entropy is None:
+        raise ValueError("g_entropy needs entropy")
+    L.check(load().quip_logprobs_backward(
+        x, _dtype(logits), T, V, _row_stride(logits),
+        None if tokens is None else _here("tokens", tokens, _I32, (T,), dev),
+        _here("lse", lse, _F32, (T,), dev),
+        None if entropy is None else _here("entropy", entropy, _F32, (T,), dev),
+        None if g_logprob is None else _here("g_logprob", g_logprob, _F32, (T,), dev),
+        None if g_entropy is None else _here("g_entropy", g_entropy, _F32, (T,), dev),
+        d, _row_stride(d_logits), _s(stream)), "quip_logprobs_backward")
+
+
+@dataclass
+class TokenScores:
+    logprob: torch.Tensor        # T fp32, 0 where no token is given
+    entropy: torch.Tensor        # T fp32
+    lse: torch.Tensor            # T fp32
+    top_values: Optional[torch.Tensor] = None    # T x k fp32
+    top_ids: Optional[torch.Tensor] = None       # T x k int32
 
 
 def quip_dequantize(codes: torch.Tensor, lo: torch.Tensor, scale: torch.Tensor, W_hat_t: torch.Tensor,

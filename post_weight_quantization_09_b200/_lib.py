@@ -16,6 +16,7 @@ QUIP_T_IDENTITY, QUIP_T_HADAMARD, QUIP_T_KRONECKER = 0, 1, 2
 QUIP_T_PERMUTE = 0x100
 QUIP_OP_INCOHERENCE_FORWARD, QUIP_OP_INCOHERENCE_INVERSE, QUIP_OP_LDL, QUIP_OP_LDLQ = 0, 1, 2, 3
 QUIP_OP_GREEDY, QUIP_OP_QMATVEC = 4, 5
+QUIP_LOGPROBS_MAX_TOP = 32
 
 # name -> (restype, argtypes); the list of every symbol include/quip.h declares
 SIGNATURES = {
@@ -52,6 +53,10 @@ SIGNATURES = {
     "quip_pack_codes": (c_int, [c_void_p, c_int64, c_int64, c_int, c_void_p, c_int64, c_void_p]),
     "quip_qmatvec": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int, c_void_p, c_int,
                              c_int64, c_int64, c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
+    "quip_logprobs": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
+                              c_int, c_void_p, c_void_p, c_void_p]),
+    "quip_logprobs_backward": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                       c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),
     "quip_dequantize": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
     "quip_workspace_size": (c_int, [c_int, c_void_p, c_int64, c_int64, c_int64, POINTER(c_size_t)]),
     "quip_quantize_layer": (c_int, [c_void_p, c_uint64, c_void_p, c_int, c_int64, c_void_p, c_int, c_int64,

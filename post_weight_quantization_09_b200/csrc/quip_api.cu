@@ -17,6 +17,7 @@
 #include "hessian.cuh"
 #include "ldl.cuh"
 #include "ldlq.cuh"
+#include "logprobs.cuh"
 #include "rng.cuh"
 #include "rounding.cuh"
 #include "qmatvec.cuh"
@@ -195,6 +196,25 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Launch as clusters of `cluster` CTAs (grid.x a multiple of it).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                           cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
@@ -1830,6 +1850,97 @@ quip_status quip_qmatvec(const quip_transform* tf, const uint32_t* packed, int64
   } else {
     QCHECK(side_rows<float>(U, true, z, m, y, B, tmp, st));
   }
+  return QUIP_OK;
+}
+
+}  // extern "C"
+
+namespace {
+// CTAs per row: more where the rows leave SMs idle (k_logprobs keeps four
+// CTAs on an SM) and each still gets a few thousand logits.
+unsigned logprobs_cluster(int64_t T, int64_t V) {
+  unsigned nc = 1;
+  while (nc < lp::MAX_CLUSTER && T * nc * 2 <= 4 * (int64_t)num_sms() && V / (nc * 2) >= 4096) nc *= 2;
+  return nc;
+}
+
+template <typename TX>
+cudaError_t logprobs_launch(const void* logits, int64_t T, int64_t V, int64_t ld, const int32_t* tokens,
+                            float* logprob, float* entropy, float* lse, int k, float* top_values,
+                            int32_t* top_ids, cudaStream_t st) {
+  const unsigned nc = logprobs_cluster(T, V);
+  const TX* x = static_cast<const TX*>(logits);
+  LaunchScope ls("k_logprobs", st);
+  return k > 0 ? launch_cluster(lp::k_logprobs<TX, true>, (unsigned)T * nc, lp::NT, 0, nc, st, x, ld, (int)V, tokens,
+                                logprob, entropy, lse, k, top_values, top_ids)
+               : launch_cluster(lp::k_logprobs<TX, false>, (unsigned)T * nc, lp::NT, 0, nc, st, x, ld, (int)V, tokens,
+                                logprob, entropy, lse, k, top_values, top_ids);
+}
+
+template <typename TX>
+cudaError_t logprobs_grad_launch(const void* logits, int64_t T, int64_t V, int64_t ld, const int32_t* tokens,
+                                 const float* lse, const float* entropy, const float* g_logprob,
+                                 const float* g_entropy, void* d_logits, int64_t ldd, cudaStream_t st) {
+  const int nseg = (int)((V + lp::grad_cols<TX>() - 1) / lp::grad_cols<TX>());
+  LaunchScope ls("k_logprobs_grad", st);
+  lp::k_logprobs_grad<TX><<<(unsigned)(T * nseg), lp::NT, 0, st>>>(static_cast<const TX*>(logits), ld, (int)V, tokens,
+                                                                   lse, entropy, g_logprob, g_entropy,
+                                                                   static_cast<TX*>(d_logits), ldd, nseg);
+  return cudaGetLastError();
+}
+
+// T rows of V logits, row stride ld: at most 2^28 logits a row, 2^22 rows.
+quip_status logits_shape(int64_t T, int64_t V, int64_t ld) {
+  return T < 0 || V < 1 || ld < V || V > (int64_t(1) << 28) || T > (int64_t(1) << 22) ||
+                 T * ((V + 4095) / 4096) > INT32_MAX
+             ? QUIP_ERR_SHAPE
+             : QUIP_OK;
+}
+}  // namespace
+
+extern "C" {
+
+quip_status quip_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int32_t* tokens,
+                          float* logprob, float* entropy, float* lse, int k, float* top_values, int32_t* top_ids,
+                          void* stream) {
+  if (dtype != QUIP_F32 && dtype != QUIP_BF16) return QUIP_ERR_ARG;
+  if (k < 0 || k > QUIP_LOGPROBS_MAX_TOP || (tokens != nullptr) != (logprob != nullptr)) return QUIP_ERR_ARG;
+  quip_status s = logits_shape(T, V, ld);
+  if (s != QUIP_OK) return s;
+  if (k > V) return QUIP_ERR_SHAPE;
+  if (T == 0) return QUIP_OK;
+  if (!logits || (k > 0 && (!top_values || !top_ids))) return QUIP_ERR_ARG;
+  cudaStream_t st = S(stream);
+  QCHECK(dtype == QUIP_BF16
+             ? logprobs_launch<__nv_bfloat16>(logits, T, V, ld, tokens, logprob, entropy, lse, k, top_values, top_ids, st)
+             : logprobs_launch<float>(logits, T, V, ld, tokens, logprob, entropy, lse, k, top_values, top_ids, st));
+  return QUIP_OK;
+}
+
+quip_status quip_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                   const int32_t* tokens, const float* lse, const float* entropy,
+                                   const float* g_logprob, const float* g_entropy, void* d_logits, int64_t ldd,
+                                   void* stream) {
+  if (dtype != QUIP_F32 && dtype != QUIP_BF16) return QUIP_ERR_ARG;
+  if ((g_logprob && !tokens) || (g_entropy && !entropy)) return QUIP_ERR_ARG;
+  quip_status s = logits_shape(T, V, ld);
+  if (s != QUIP_OK) return s;
+  if (ldd < V) return QUIP_ERR_SHAPE;
+  if (T == 0) return QUIP_OK;
+  if (!logits || !lse || !d_logits) return QUIP_ERR_ARG;
+  if (logits == d_logits) {
+    if (ld != ldd) return QUIP_ERR_ARG;
+  } else {
+    const uintptr_t e = dtype == QUIP_BF16 ? 2 : 4, a = reinterpret_cast<uintptr_t>(logits),
+                    b = reinterpret_cast<uintptr_t>(d_logits);
+    if (a < b + ((T - 1) * ldd + V) * e && b < a + ((T - 1) * ld + V) * e) return QUIP_ERR_ARG;
+  }
+  cudaStream_t st = S(stream);
+  QCHECK(dtype == QUIP_BF16
+             ? logprobs_grad_launch<__nv_bfloat16>(logits, T, V, ld, tokens, lse, entropy, g_logprob, g_entropy,
+                                                   d_logits, ldd, st)
+             : logprobs_grad_launch<float>(logits, T, V, ld, tokens, lse, entropy, g_logprob, g_entropy, d_logits, ldd,
+                                           st));
   return QUIP_OK;
 }
 
