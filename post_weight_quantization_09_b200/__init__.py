@@ -48,6 +48,10 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _raw_stream(stream: Optional[torch.cuda.Stream]) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
 def _s(stream: Optional[torch.cuda.Stream]):
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
@@ -66,27 +70,26 @@ def _cuda(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
-def _here(name: str, t: torch.Tensor, dtypes, shape, device=None, rows: bool = False) -> int:
-    """The address of t, once it is a tensor of one of ``dtypes`` and of
-    ``shape`` (None: any size) on the current device, with contiguous rows
-    (``rows``: any row stride) or contiguous altogether."""
+def _here(name: str, t: torch.Tensor, dtypes, shape, device: int, rows: bool = False) -> int:
+    """The address of t, once it is a tensor on ``device`` (the current one)
+    of one of ``dtypes`` and of ``shape``, contiguous or, with ``rows``, with
+    contiguous rows."""
+    if t.get_device() != device or t.dtype not in dtypes or t.shape != shape or \
+            not (t.is_contiguous() or rows and t.stride(1) == 1 and (t.shape[0] == 1 or t.stride(0) >= t.shape[1])):
+        _refuse(name, t, dtypes, shape, device, rows)
+    return t.data_ptr()
+
+
+def _refuse(name, t, dtypes, shape, device, rows):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != (torch.cuda.current_device() if device is None else device):
+    if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != s for s, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         f"{tuple('any' if w is None else w for w in shape)}")
-    if rows:
-        if t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must have contiguous rows")
-        if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-            raise ValueError(f"{name} has overlapping rows")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must have contiguous rows that do not overlap" if rows else f"{name} must be contiguous")
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -412,7 +415,7 @@ def quip_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], logprob:
     probabilities with their indices (top_values, top_ids: T x k), in one pass
     (include/quip.h)."""
     T, V = logits.shape
-    dev = torch.cuda.current_device() if logits.is_cuda else None
+    dev = torch.cuda.current_device() if logits.is_cuda else -2
     x = _here("logits", logits, _FLOATS, (T, V), dev, rows=True)
     if (tokens is None) != (logprob is None):
         raise ValueError("tokens and logprob go together")
@@ -426,7 +429,7 @@ def quip_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], logprob:
         None if entropy is None else _here("entropy", entropy, _F32, (T,), dev),
         None if lse is None else _here("lse", lse, _F32, (T,), dev), k,
         None if k == 0 else _here("top_values", top_values, _F32, (T, k), dev),
-        None if k == 0 else _here("top_ids", top_ids, _I32, (T, k), dev), _s(stream)), "quip_logprobs")
+        None if k == 0 else _here("top_ids", top_ids, _I32, (T, k), dev), _raw_stream(stream)), "quip_logprobs")
 
 
 def quip_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor], lse: torch.Tensor,
@@ -436,7 +439,7 @@ def quip_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor],
     """d_logits = the gradient of sum_t g_logprob[t] logprob[t] + g_entropy[t]
     entropy[t] with respect to the logits; d_logits may be the logits."""
     T, V = logits.shape
-    dev = torch.cuda.current_device() if logits.is_cuda else None
+    dev = torch.cuda.current_device() if logits.is_cuda else -2
     x = _here("logits", logits, _FLOATS, (T, V), dev, rows=True)
     d = _here("d_logits", d_logits, (logits.dtype,), (T, V), dev, rows=True)
     if g_logprob is not None and tokens is None:
@@ -450,7 +453,8 @@ def quip_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor],
         None if entropy is None else _here("entropy", entropy, _F32, (T,), dev),
         None if g_logprob is None else _here("g_logprob", g_logprob, _F32, (T,), dev),
         None if g_entropy is None else _here("g_entropy", g_entropy, _F32, (T,), dev),
-        d, _row_stride(d_logits), _s(stream)), "quip_logprobs_backward")
+        d, _row_stride(d_logits), _raw_stream(stream)),
+        "quip_logprobs_backward")
 
 
 @dataclass

@@ -2,12 +2,15 @@
 // and their gradient: what the logits of a quantised output layer are scored
 // by (perplexity is exp of minus the mean log probability).
 //
-// For a row x of V logits, in base 2 with t = x log2 e and T = max t:
+// For a row x of V logits, in base 2 with t = x log2 e and T the row's
+// largest t:
 //   s = sum 2^(t - T),  w = sum 2^(t - T) (t - T)
 //   lse = ln 2 (T + log2 s),  logprob = ln 2 ((t_tok - T) - log2 s),
 //   entropy = -sum p ln p = ln 2 (log2 s - w / s).
 // (T, s, w) of two parts of a row combine by scaling both to the larger T,
-// so one pass over the logits is enough.  T, s and w are fp32.
+// so one pass over the logits is enough.  All three are fp32; t - T is one
+// fused multiply-add, so its error is half a step of the difference and
+// |x| 2^-26 from log2 e's own rounding.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -21,11 +24,12 @@ namespace cg = cooperative_groups;
 
 constexpr int NT = 256;            // threads per CTA
 constexpr int GROUPS = 64;         // groups of threads whose maxima bound the k-th value; >= MAX_K
-constexpr int MAX_K = 32;
-constexpr int CAP = NT;            // candidates ranked in one step
+constexpr int MAX_K = QUIP_LOGPROBS_MAX_TOP;
+constexpr int CAP = 256;           // candidates ranked by counting; >= MAX_CLUSTER * MAX_K
 constexpr int MAX_CLUSTER = 8;
 constexpr int UNROLL = 4;          // 16-byte loads in flight per thread
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float NEG_INF = -__builtin_huge_valf();
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -37,18 +41,19 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
-constexpr float NEG_INF = -__builtin_huge_valf();
-
-// fp32 -> unsigned with the same order (-inf < ... < +inf < NaN); 0 is below all.
-// -0 counts as +0, so that equal logits stay equal.
+// fp32 <-> unsigned with the same order (-inf < ... < +inf < NaN); 0 is below
+// all.  -0 counts as +0, so that equal logits stay equal.
 __device__ __forceinline__ uint32_t order_key(float x) {
-  if (x == 0.f) x = 0.f;
-  const uint32_t u = __float_as_uint(x);
   if (x != x) return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
 
-// The logits of one 16-byte vector as fp32.
+// The logits of one 16-byte vector: as pairs of fp32, and their maximum
+// (NaN only where every logit is).
 template <typename TX> struct Vec;
 template <> struct Vec<float> {
   static constexpr int N = 4;
@@ -56,6 +61,22 @@ template <> struct Vec<float> {
   static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
     f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
     f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  }
+  // every logit at least `floor`; a NaN stays
+  static __device__ __forceinline__ void hold(uint4& v, float floor) {
+    v.x = __float_as_uint(max_nan(__uint_as_float(v.x), floor));
+    v.y = __float_as_uint(max_nan(__uint_as_float(v.y), floor));
+    v.z = __float_as_uint(max_nan(__uint_as_float(v.z), floor));
+    v.w = __float_as_uint(max_nan(__uint_as_float(v.w), floor));
+  }
+  template <int K>
+  static __device__ __forceinline__ float top(const uint4 (&v)[K]) {
+    float t = NEG_INF;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      t = fmaxf(t, fmaxf(fmaxf(__uint_as_float(v[j].x), __uint_as_float(v[j].y)),
+                         fmaxf(__uint_as_float(v[j].z), __uint_as_float(v[j].w))));
+    return t;
   }
 };
 template <> struct Vec<__nv_bfloat16> {
@@ -69,48 +90,94 @@ template <> struct Vec<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
   }
+  static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t u) {
+    return *reinterpret_cast<const __nv_bfloat162*>(&u);
+  }
+  static __device__ __forceinline__ void hold(uint4& v, float floor) {
+    const __nv_bfloat162 f = __float2bfloat162_rn(floor);
+    uint32_t* u[4] = {&v.x, &v.y, &v.z, &v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 r = __hmax2_nan(pair(*u[i]), f);
+      *u[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+  template <int K>
+  static __device__ __forceinline__ float top(const uint4 (&v)[K]) {
+    __nv_bfloat162 t = pair(PAD);
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      t = __hmax2(t, __hmax2(__hmax2(pair(v[j].x), pair(v[j].y)), __hmax2(pair(v[j].z), pair(v[j].w))));
+    return fmaxf(__low2float(t), __high2float(t));
+  }
 };
 
-// Running (T, s, w) of a part of a row.
+constexpr float LOW_T = 4096.f;
+
+// (T, s, w) of a part of a row.  T = -inf: no logit that 2^(t - T) can serve
+// (none above -inf, or all near the type's lowest value), s = w = 0, or NaN
+// where it met one.
 struct Part {
-  float T = NEG_INF, s = 0.f, w = 0.f;
-  // scale to the maximum T2 >= T.  A part without a finite logit (T = -inf)
-  // has s = w = 0, or NaN where it met one: kept as it is.
-  __device__ __forceinline__ void raise(float T2) {
-    const float d = T == NEG_INF ? 0.f : T - T2;
+  float T, s, w;
+  __device__ __forceinline__ void raise(float to) {     // to >= T
+    const float d = T == NEG_INF ? 0.f : T - to;
     const float f = ex2(d);
     w = f * fmaf(d, s, w);
     s *= f;
-    T = T2;
+    T = to;
   }
-  __device__ __forceinline__ void add(Part o) {
-    const float T2 = fmaxf(T, o.T);
-    raise(T2);
-    o.raise(T2);
-    s += o.s, w += o.w;
+};
+__device__ __forceinline__ Part no_part() { return Part{NEG_INF, 0.f, 0.f}; }
+
+// The combination of the 32 lanes' parts, in every lane.
+__device__ __forceinline__ Part warp_combine(Part p) {
+  // an ordered key for redux.sync; a maximum is never NaN
+  p.raise(key_value(__reduce_max_sync(0xffffffffu, order_key(p.T))));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    p.s += __shfl_xor_sync(0xffffffffu, p.s, o);
+    p.w += __shfl_xor_sync(0xffffffffu, p.w, o);
+  }
+  return p;
+}
+
+// A thread's running part, with the largest logit m itself.  T follows the
+// maximum only once that is SLACK above it (2^(t - T) has room; the entropy's
+// log2 s and w / s then share up to SLACK, half a step of which is small):
+// most rounds then cost a comparison.
+constexpr float SLACK = 8.f;
+struct Running {
+  float m = NEG_INF;
+  Part p{NEG_INF, 0.f, 0.f};
+  // A logit of -inf (a barred token, padding) has e = 0, but t - T = -inf
+  // would make e (t - T) NaN: logits are held at a value whose exponential is
+  // 0 in fp32, at least 100 below T's after its rounding to bf16 too
+  // (lower by 1 / 64 where that is more).
+  float floor = -200.f, ref = 0.f;
+  // `top` is the maximum of the logits about to be added
+  __device__ __forceinline__ void raise(float top) {
+    m = fmaxf(m, top);
+    if (m * LOG2E > p.T + SLACK) {
+      p.raise(m * LOG2E);
+      floor = m - fmaxf(200.f, fabsf(m) * 0.015625f);
+      ref = -p.T;
+    }
+  }
+  // N more logits, held at floor
+  template <int N>
+  __device__ __forceinline__ void add(const float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float d = fmaf(x[i], LOG2E, ref), e = ex2(d);
+      p.s += e;
+      p.w = fmaf(e, d, p.w);
+    }
   }
 };
 
-// N more logits.  A -inf logit (and padding) counts 0: its exponent is held
-// at -200, where 2^x is 0 in fp32; max.NaN lets a NaN through.
-template <int N>
-__device__ __forceinline__ void accumulate(Part& p, const float (&f)[N]) {
-  float top = f[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) top = fmaxf(top, f[i]);
-  p.raise(fmaxf(p.T, top * LOG2E));
-  const float T = p.T == NEG_INF ? 0.f : p.T;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float d = max_nan(fmaf(f[i], LOG2E, -T), -200.f);
-    const float e = ex2(d);
-    p.s += e;
-    p.w = fmaf(e, d, p.w);
-  }
-}
-
 // The part of a row that a CTA handles: logits [v0, v1), of which the first
-// `head` come before the first 16-byte boundary and `tail` after the last.
+// `head` come before the first 16-byte boundary and `tail` after the last
+// vector.  Thread t reads vectors t, t + NT, ... and edge logits t.
 template <typename TX>
 struct Slice {
   const TX* x;                     // the row
@@ -128,16 +195,44 @@ struct Slice {
     if (which == 0) return tid < head ? v0 + tid : -1;
     return tid < tail ? v1 - tail + tid : -1;
   }
+  __device__ __forceinline__ bool mine(int tid) const { return tid < nvec || tid < head || tid < tail; }
+  // fn(logit, index) for those of thread t's logits that are not below
+  // `least` (all NaN among them), of step c: its c-th vector, or past the
+  // last its edge logits
+  __device__ __forceinline__ int steps() const { return (nvec + NT - 1) / NT + 1; }
+  template <typename Fn>
+  __device__ __forceinline__ void step(int t, int c, float least, Fn fn) const {
+    constexpr int N = Vec<TX>::N;
+    const int i = t + c * NT;
+    if (c == steps() - 1) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int v = edge(e, t);
+        if (v >= 0 && !(to_f32(x[v]) < least)) fn(to_f32(x[v]), v);
+      }
+    } else if (i < nvec) {
+      float f[N];
+      Vec<TX>::unpack(__ldg(vecs() + i), f);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (!(f[j] < least)) fn(f[j], v0 + head + i * N + j);
+    }
+  }
 };
 
-struct Shared {
-  Part part[NT / 32];
-  Part cta;                        // read by the other CTAs of the cluster
-  uint32_t gmax[GROUPS];
+// What the threads that stream a row's slice leave for the rest.
+struct RowShared {
+  Part part[NT / 32];                          // per warp
+  uint32_t gmax[GROUPS];                       // order_key of the groups' maxima, 0: none
+};
+// Choosing the top alternatives.
+struct TopShared {
   uint32_t tau;
-  int count;
-  unsigned long long cand[CAP];    // (order_key << 32) | ~index: larger = earlier
-  unsigned long long best[MAX_K];  // the CTA's k largest, in order; read by the cluster
+  int count, owners;
+  int owner[NT];
+  // (order_key << 32) | ~index: larger = earlier
+  alignas(16) unsigned long long cand[CAP];
+  alignas(16) unsigned long long best[MAX_K];  // the slice's k largest, in order
   unsigned long long red[NT / 32];
 };
 
@@ -145,199 +240,252 @@ __device__ __forceinline__ unsigned long long cand_key(float x, int v) {
   return ((unsigned long long)order_key(x) << 32) | (uint32_t)~(uint32_t)v;
 }
 
-// Calls fn(logit, index) for every logit of the slice that thread `owner`
-// read, the lanes of the calling warp sharing its vectors.
-template <typename TX, typename Fn>
-__device__ __forceinline__ void warp_for_owner(const Slice<TX>& sl, int owner, int lane, Fn fn) {
-  constexpr int N = Vec<TX>::N;
-  for (int i = owner + lane * NT; i < sl.nvec; i += 32 * NT) {
-    float f[N];
-    Vec<TX>::unpack(sl.vecs()[i], f);
-#pragma unroll
-    for (int j = 0; j < N; ++j) fn(f[j], sl.v0 + sl.head + i * N + j);
+// How many of list[0 .. count) are above c; list is 16-byte aligned.
+__device__ __forceinline__ int count_above(const unsigned long long* list, int count, unsigned long long c) {
+  const ulonglong2* two = reinterpret_cast<const ulonglong2*>(list);
+  int above = 0;
+#pragma unroll 8
+  for (int i = 0; i < count / 2; ++i) {
+    const ulonglong2 v = two[i];
+    above += (v.x > c ? 1 : 0) + (v.y > c ? 1 : 0);
   }
-  if (lane < 2) {
-    const int v = sl.edge(lane, owner);
-    if (v >= 0) fn(to_f32(sl.x[v]), v);
-  }
+  if (count & 1) above += list[count - 1] > c ? 1 : 0;
+  return above;
 }
 
-// The k largest (value, then lowest index) logits of the CTA's slice into
-// sh.best, in order; keys of 0 where the slice has fewer.  tmax is the
-// largest logit the thread read (-inf if none).
+// A barrier of the NT threads that read logits.
+__device__ __forceinline__ void team_sync() { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); }
+
+// The k largest (value, then lowest index) logits of a slice into tp.best, in
+// order; keys of 0 where the slice has fewer.  tid: the thread's number in
+// the team.
 //
-// The k-th largest of the 64 groups' maxima is at most the k-th largest
-// logit, and few logits are above it (about 64 ln(64 / (64 - k)) of a random
-// row), all in threads whose own maximum is: those threads' logits are read
-// again (from L2) and the ones not below are ranked by counting.  Where more
-// than CAP pass (many equal maxima, or most of them in one thread), k rounds
-// of a maximum over all logits below the one before do the same.
+// The k-th largest of the groups' maxima is at most the k-th largest logit,
+// and few logits are above it (about 64 ln(64 / (64 - k)) of a random row),
+// all in threads whose own maximum is: those threads' logits are read again
+// (from L2) and the ones not below are ranked by counting.  Where more than
+// CAP pass (many equal maxima, or most of them in one thread), k rounds of a
+// maximum over all logits below the one before find the same.
 template <typename TX>
-__device__ void cta_top(Shared& sh, const Slice<TX>& sl, float tmax, bool any, int k) {
+__device__ __forceinline__ void choose_top(TopShared& tp, const RowShared& rs, const Slice<TX>& sl, float tmax, int k) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < GROUPS) sh.gmax[tid] = 0u;
-  if (tid < MAX_K) sh.best[tid] = 0ull;
-  if (tid == 0) sh.count = 0, sh.tau = 0u;
-  __syncthreads();
-  const uint32_t mine = any ? order_key(tmax) : 0u;
-  if (any) atomicMax(&sh.gmax[tid % GROUPS], mine);
-  __syncthreads();
-  if (tid < GROUPS) {
-    const uint32_t g = sh.gmax[tid];
-    int above = 0;
-    for (int i = 0; i < GROUPS; ++i) {
-      const uint32_t o = sh.gmax[i];
-      above += (o > g || (o == g && i < tid)) ? 1 : 0;
+  if (warp == 0) {
+    // the k-th largest of the 64, two per lane: the largest leaves k times
+    uint32_t hi = rs.gmax[lane], lo = rs.gmax[lane + 32], top = 0u;
+    if (lo > hi) { const uint32_t c = hi; hi = lo, lo = c; }
+    for (int j = 0; j < k; ++j) {
+      top = __reduce_max_sync(0xffffffffu, hi);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, hi == top)) - 1) hi = lo, lo = 0u;
     }
-    if (above == k - 1) sh.tau = g;
+    if (lane == 0) tp.tau = top;
   }
-  __syncthreads();
-  const uint32_t tau = sh.tau;
-  unsigned todo = __ballot_sync(0xffffffffu, any && mine >= tau);
-  while (todo) {
-    const int b = __ffs(todo) - 1;
-    todo &= todo - 1;
-    warp_for_owner(sl, warp * 32 + b, lane, [&](float f, int v) {
-      if (order_key(f) >= tau) {
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < CAP) sh.cand[at] = cand_key(f, v);
-      }
-    });
-  }
-  __syncthreads();
-  const int count = sh.count;
+  team_sync();
+  const uint32_t tau = tp.tau;
+  if (sl.mine(tid) && order_key(tmax) >= tau) tp.owner[atomicAdd(&tp.owners, 1)] = tid;
+  team_sync();
+  const int steps = sl.steps();
+  const float least = tau ? key_value(tau) : NEG_INF;
+  for (int i = warp; i < tp.owners; i += NT / 32)
+    for (int c = lane; c < steps; c += 32)
+      sl.step(tp.owner[i], c, least, [&](float f, int v) {
+        const int at = atomicAdd(&tp.count, 1);
+        if (at < CAP) tp.cand[at] = cand_key(f, v);
+      });
+  team_sync();
+  const int count = tp.count;
   if (count <= CAP) {
-    if (tid < count) {
-      const unsigned long long c = sh.cand[tid];
-      int above = 0;
-      for (int i = 0; i < count; ++i) above += sh.cand[i] > c ? 1 : 0;
-      if (above < k) sh.best[above] = c;
+    for (int i = tid; i < count; i += NT) {
+      const unsigned long long c = tp.cand[i];
+      const int above = count_above(tp.cand, count, c);
+      if (above < k) tp.best[above] = c;
     }
-    __syncthreads();
+    team_sync();
     return;
   }
   unsigned long long last = ~0ull;
   for (int j = 0; j < k; ++j) {
     unsigned long long top = 0ull;
-    for (int own = 0; own < 32; ++own)
-      warp_for_owner(sl, warp * 32 + own, lane, [&](float f, int v) {
-        const unsigned long long c = cand_key(f, v);
-        if (c < last && c > top) top = c;
+    for (int c = 0; c < steps; ++c)
+      sl.step(tid, c, NEG_INF, [&](float f, int v) {
+        const unsigned long long key = cand_key(f, v);
+        if (key < last && key > top) top = key;
       });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const unsigned long long c = __shfl_xor_sync(0xffffffffu, top, o);
       top = c > top ? c : top;
     }
-    if (lane == 0) sh.red[warp] = top;
-    __syncthreads();
+    if (lane == 0) tp.red[warp] = top;
+    team_sync();
     top = 0ull;
-    for (int i = 0; i < NT / 32; ++i) top = sh.red[i] > top ? sh.red[i] : top;
-    if (tid == 0) sh.best[j] = top;
+    for (int i = 0; i < NT / 32; ++i) top = tp.red[i] > top ? tp.red[i] : top;
+    if (tid == 0) tp.best[j] = top;
     last = top;
-    __syncthreads();
+    team_sync();
   }
+}
+
+// For the rows whose largest |t| is LOW_T or more, where half a step of T no
+// longer is small (and of a maximum of the type's lowest value, -inf or +inf): their maximum m, and the sums of exp and
+// of exp (x - m) with the differences in natural units, held at -200; one
+// warp.
+template <typename TX>
+__device__ __noinline__ Part sum_low(const TX* x, int V) {
+  float m = NEG_INF;
+  for (int v = threadIdx.x % 32; v < V; v += 32) m = fmaxf(m, to_f32(x[v]));
+  m = warp_max(m);
+  const float ref = m == NEG_INF ? 0.f : m;
+  Part p{m, 0.f, 0.f};
+  for (int v = threadIdx.x % 32; v < V; v += 32) {
+    const float d = max_nan(to_f32(x[v]) - ref, -200.f), e = ex2(d * LOG2E);
+    p.s += e;
+    p.w = fmaf(e, d, p.w);
+  }
+  p.s = warp_sum(p.s), p.w = warp_sum(p.w);
+  return p;
+}
+
+struct Args {
+  int64_t ld;
+  int V, k;
+  int64_t T;
+  const int32_t* tokens;
+  float *logprob, *entropy, *lse, *top_values;
+  int32_t* top_ids;
+};
+
+// A row's outputs from its parts' combination, and the log probability of a
+// logit of the row.
+template <typename TX>
+struct Finish {
+  const TX* x;
+  Part p;
+  float log_s;                 // in the units of p: base 2, or natural for a row of sum_low
+  bool low;
+  // every thread of a warp; p from warp_combine
+  __device__ __forceinline__ Finish(const TX* x_, int V, Part p_) : x(x_), p(p_), low(!(fabsf(p_.T) < LOW_T)) {
+    if (low) p = sum_low(x, V);
+    log_s = low ? logf(p.s) : log2f(p.s);
+  }
+  __device__ __forceinline__ bool empty() const { return p.T == NEG_INF && p.s == 0.f; }   // no logit above -inf
+  __device__ __forceinline__ float given(int v) const {
+    const float f = to_f32(x[v]);
+    if (low) return empty() ? NEG_INF : (f - p.T) - log_s;
+    if (f < -1e38f) return f - LN2 * (p.T + log_s);      // times log2 e it may leave fp32
+    return LN2 * (fmaf(f, LOG2E, -p.T) - log_s);
+  }
+  __device__ __forceinline__ void write(const Args& a, int64_t row) const {
+    const float unit = low ? 1.f : LN2;
+    if (a.lse) a.lse[row] = empty() ? NEG_INF : unit * (p.T + log_s);
+    if (a.entropy) a.entropy[row] = empty() ? 0.f : unit * (log_s - p.w / p.s);
+    if (a.tokens) {
+      const int tok = a.tokens[row];
+      if (tok >= a.V || tok < -1) record_status(QUIP_ERR_ARG);
+      a.logprob[row] = tok >= 0 && tok < a.V ? given(tok) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void write_top(const Args& a, int64_t row, int at, unsigned long long c) const {
+    const int v = (int)~(uint32_t)c;
+    a.top_ids[row * a.k + at] = v;
+    a.top_values[row * a.k + at] = given(v);
+  }
+};
+
+template <typename TX, int K>
+__device__ __forceinline__ void consume(Running& r, uint4 (&u)[K]) {
+  constexpr int N = Vec<TX>::N;
+  r.raise(Vec<TX>::top(u));
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    float f[N];
+    Vec<TX>::hold(u[j], r.floor);
+    Vec<TX>::unpack(u[j], f);
+    r.add(f);
+  }
+}
+// This thread's vectors (every NT-th) of the `n` at v, CHUNK at most.
+constexpr int CHUNK = UNROLL * NT;
+template <typename TX>
+__device__ __forceinline__ void consume_chunk(Running& r, const uint4* v, int n, int tid) {
+  if (n >= CHUNK) {
+    uint4 u[UNROLL];
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j) u[j] = v[tid + j * NT];
+    consume<TX>(r, u);
+  } else {
+    uint4 u[UNROLL];
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j) {
+      constexpr uint32_t P = Vec<TX>::PAD;
+      u[j] = tid + j * NT < n ? v[tid + j * NT] : make_uint4(P, P, P, P);
+    }
+    consume<TX>(r, u);
+  }
+}
+// The thread's edge logits, then its and its warp's part into rs.
+template <typename TX, bool TOP>
+__device__ __forceinline__ void close_row(Running& r, const Slice<TX>& sl, RowShared& rs, TopShared& tp, int tid) {
+  if (TOP && tid == 0) tp.count = 0, tp.owners = 0;
+  const int a = sl.edge(0, tid), b = sl.edge(1, tid);
+  if (a >= 0 || b >= 0) {
+    float f[2] = {a >= 0 ? to_f32(sl.x[a]) : NEG_INF, b >= 0 ? to_f32(sl.x[b]) : NEG_INF};
+    r.raise(fmaxf(f[0], f[1]));
+      f[0] = max_nan(f[0], r.floor), f[1] = max_nan(f[1], r.floor);
+    r.add(f);
+  }
+  if (TOP && sl.mine(tid)) atomicMax(&rs.gmax[tid % GROUPS], order_key(r.m));
+  const Part p = warp_combine(r.p);
+  if (tid % 32 == 0) rs.part[tid / 32] = p;
 }
 
 // One cluster per row (one CTA where the rows fill the GPU, up to 8 where
 // they do not), each CTA a slice of it; the first CTA combines.
 template <typename TX, bool TOP>
-__global__ void __launch_bounds__(NT, 4)
-    k_logprobs(const TX* __restrict__ logits, int64_t ld, int V, const int32_t* __restrict__ tokens,
-               float* __restrict__ logprob, float* __restrict__ entropy, float* __restrict__ lse, int k,
-               float* __restrict__ top_values, int32_t* __restrict__ top_ids) {
+__global__ void __launch_bounds__(NT, 5) k_logprobs(const TX* __restrict__ logits, const __grid_constant__ Args a) {
   constexpr int N = Vec<TX>::N;
-  __shared__ Shared sh;
+  __shared__ RowShared rs;
+  __shared__ TopShared tp;
+  __shared__ Part cta;                         // read by the other CTAs of the cluster, as tp.best
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
   const int64_t row = blockIdx.x / nc;
-  const TX* x = logits + row * ld;
+  const TX* x = logits + row * a.ld;
   // slices of whole 16-byte vectors' worth of logits
-  const int per = ((V + nc - 1) / nc + N - 1) / N * N;
-  const Slice<TX> sl(x, min(V, rank * per), min(V, (rank + 1) * per));
-
-  Part p;
-  float tmax = NEG_INF;
-  const uint4* vecs = sl.vecs();
-  for (int i = tid; i < sl.nvec; i += UNROLL * NT) {
-    uint4 u[UNROLL];
-#pragma unroll
-    for (int j = 0; j < UNROLL; ++j) {
-      constexpr uint32_t P = Vec<TX>::PAD;
-      u[j] = i + j * NT < sl.nvec ? __ldg(vecs + i + j * NT) : make_uint4(P, P, P, P);
-    }
-    float f[UNROLL * N];
-#pragma unroll
-    for (int j = 0; j < UNROLL; ++j) Vec<TX>::unpack(u[j], f + j * N);
-    if (TOP) {
-#pragma unroll
-      for (int j = 0; j < UNROLL * N; ++j) tmax = fmaxf(tmax, f[j]);
-    }
-    accumulate(p, f);
+  const int per = ((a.V + nc - 1) / nc + N - 1) / N * N;
+  const Slice<TX> sl(x, min(a.V, rank * per), min(a.V, (rank + 1) * per));
+  if (TOP) {
+    if (tid < GROUPS) rs.gmax[tid] = 0u;
+    if (tid < MAX_K) tp.best[tid] = 0ull;
+    __syncthreads();
   }
-  {
-    const int a = sl.edge(0, tid), b = sl.edge(1, tid);
-    const float f[2] = {a >= 0 ? to_f32(x[a]) : NEG_INF, b >= 0 ? to_f32(x[b]) : NEG_INF};
-    if (a >= 0 || b >= 0) {
-      tmax = fmaxf(tmax, fmaxf(f[0], f[1]));
-      accumulate(p, f);
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Part q;
-    q.T = __shfl_xor_sync(0xffffffffu, p.T, o);
-    q.s = __shfl_xor_sync(0xffffffffu, p.s, o);
-    q.w = __shfl_xor_sync(0xffffffffu, p.w, o);
-    p.add(q);
-  }
-  if (lane == 0) sh.part[warp] = p;
-  if constexpr (TOP) cta_top(sh, sl, tmax, tid < sl.nvec || tid < sl.head || tid < sl.tail, k);
+  Running r;
+  for (int i = 0; i < sl.nvec; i += CHUNK) consume_chunk<TX>(r, sl.vecs() + i, sl.nvec - i, tid);
+  close_row<TX, TOP>(r, sl, rs, tp, tid);
   __syncthreads();
-  if (tid == 0) {
-    Part c = sh.part[0];
-    for (int i = 1; i < NT / 32; ++i) c.add(sh.part[i]);
-    sh.cta = c;
+  if (warp == NT / 32 - 1) {
+    const Part p = warp_combine(lane < NT / 32 ? rs.part[lane] : no_part());
+    if (lane == 0) cta = p;
   }
+  if constexpr (TOP) choose_top(tp, rs, sl, r.m, k);
   if (nc > 1) cluster.sync();
   else __syncthreads();
   if (rank == 0) {
-    Part c = sh.cta;
-    for (int i = 1; i < nc; ++i) c.add(*cluster.map_shared_rank(&sh.cta, i));
-    const float l2 = log2f(c.s);
-    const bool empty = c.s == 0.f;                       // no logit above -inf
-    const float T = c.T == NEG_INF ? 0.f : c.T;
-    if (tid == 0) {
-      if (lse) lse[row] = empty ? NEG_INF : LN2 * (T + l2);
-      if (entropy) entropy[row] = empty ? 0.f : LN2 * (l2 - c.w / c.s);
-      if (tokens) {
-        const int tok = tokens[row];
-        float v = 0.f;
-        if (tok >= V || tok < -1) record_status(QUIP_ERR_ARG);
-        else if (tok >= 0) v = empty ? NEG_INF : LN2 * (fmaf(to_f32(x[tok]), LOG2E, -T) - l2);
-        logprob[row] = v;
-      }
-    }
+    const Finish<TX> fin(x, a.V, warp_combine(lane < nc ? *cluster.map_shared_rank(&cta, lane) : no_part()));
+    if (tid == 0) fin.write(a, row);
     if constexpr (TOP) {
-      // the nc lists of k keys, ranked by counting
-      const int total = nc * k;
-      if (nc > 1) {
-        if (tid < total) sh.cand[tid] = cluster.map_shared_rank(sh.best, tid / k)[tid % k];
+      if (nc == 1) {
+        if (tid < k) fin.write_top(a, row, tid, tp.best[tid]);
+      } else {
+        // the nc lists of k keys, ranked by counting; a key of 0 is none
+        const int total = nc * k;
+        for (int i = tid; i < total; i += NT) tp.cand[i] = cluster.map_shared_rank(tp.best, i / k)[i % k];
         __syncthreads();
-      }
-      const unsigned long long* list = nc > 1 ? sh.cand : sh.best;
-      if (tid < total) {
-        const unsigned long long c = list[tid];
-        int above = tid;
-        if (nc > 1) {
-          above = 0;
-          for (int i = 0; i < total; ++i) above += (list[i] > c || (list[i] == c && i < tid)) ? 1 : 0;
-        }
-        if (above < k) {
-          const int v = (int)~(uint32_t)c;
-          top_ids[row * k + above] = v;
-          top_values[row * k + above] = empty ? NEG_INF : LN2 * (fmaf(to_f32(x[v]), LOG2E, -T) - l2);
+        for (int i = tid; i < total; i += NT) {
+          const unsigned long long c = tp.cand[i];
+          if (c == 0ull) continue;
+          const int above = count_above(tp.cand, total, c);
+          if (above < k) fin.write_top(a, row, above, c);
         }
       }
     }

@@ -1860,21 +1860,17 @@ namespace {
 // CTAs on an SM) and each still gets a few thousand logits.
 unsigned logprobs_cluster(int64_t T, int64_t V) {
   unsigned nc = 1;
-  while (nc < lp::MAX_CLUSTER && T * nc * 2 <= 4 * (int64_t)num_sms() && V / (nc * 2) >= 4096) nc *= 2;
+  while (nc < lp::MAX_CLUSTER && T * nc * 2 <= 4 * (int64_t)num_sms() && V / (nc * 2) >= 2048) nc *= 2;
   return nc;
 }
 
 template <typename TX>
-cudaError_t logprobs_launch(const void* logits, int64_t T, int64_t V, int64_t ld, const int32_t* tokens,
-                            float* logprob, float* entropy, float* lse, int k, float* top_values,
-                            int32_t* top_ids, cudaStream_t st) {
-  const unsigned nc = logprobs_cluster(T, V);
+cudaError_t logprobs_launch(const void* logits, const lp::Args& a, cudaStream_t st) {
   const TX* x = static_cast<const TX*>(logits);
+  const unsigned nc = logprobs_cluster(a.T, a.V);
   LaunchScope ls("k_logprobs", st);
-  return k > 0 ? launch_cluster(lp::k_logprobs<TX, true>, (unsigned)T * nc, lp::NT, 0, nc, st, x, ld, (int)V, tokens,
-                                logprob, entropy, lse, k, top_values, top_ids)
-               : launch_cluster(lp::k_logprobs<TX, false>, (unsigned)T * nc, lp::NT, 0, nc, st, x, ld, (int)V, tokens,
-                                logprob, entropy, lse, k, top_values, top_ids);
+  return launch_cluster(a.k > 0 ? lp::k_logprobs<TX, true> : lp::k_logprobs<TX, false>, (unsigned)a.T * nc, lp::NT, 0,
+                        nc, st, x, a);
 }
 
 template <typename TX>
@@ -1911,9 +1907,8 @@ quip_status quip_logprobs(const void* logits, int dtype, int64_t T, int64_t V, i
   if (T == 0) return QUIP_OK;
   if (!logits || (k > 0 && (!top_values || !top_ids))) return QUIP_ERR_ARG;
   cudaStream_t st = S(stream);
-  QCHECK(dtype == QUIP_BF16
-             ? logprobs_launch<__nv_bfloat16>(logits, T, V, ld, tokens, logprob, entropy, lse, k, top_values, top_ids, st)
-             : logprobs_launch<float>(logits, T, V, ld, tokens, logprob, entropy, lse, k, top_values, top_ids, st));
+  const lp::Args a{ld, (int)V, k, T, tokens, logprob, entropy, lse, top_values, top_ids};
+  QCHECK(dtype == QUIP_BF16 ? logprobs_launch<__nv_bfloat16>(logits, a, st) : logprobs_launch<float>(logits, a, st));
   return QUIP_OK;
 }
 

@@ -124,7 +124,8 @@ def _check(x, tokens, k, got):
     def near(a, b, tol):
         live = np.isfinite(b)
         np.testing.assert_array_equal(a[~live], b[~live])
-        assert np.all(np.abs(a - b)[live] <= np.broadcast_to(tol, b.shape)[live]), np.max(np.abs(a - b)[live])
+        off = np.abs(a[live] - b[live])
+        assert np.all(off <= np.broadcast_to(tol, b.shape)[live]), np.max(off)
     near(host(got[2]), lse, rel + 4 * U * mag)
     gap = np.where(np.isfinite(lp), np.abs(lp), 0.0)
     near(host(got[0]), lp, rel + 4 * U * (mag + gap))
@@ -139,7 +140,8 @@ def _check(x, tokens, k, got):
 @gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("T,V,k", [(1, 1, 1), (1, 1, 0), (2, 7, 7), (3, 33, 32), (5, 100, 20), (1, 4095, 1),
-                                   (700, 257, 2), (4, 32000, 8), (1, 50257, 32), (9, 128000, 20), (130, 8193, 5)])
+                                   (700, 257, 2), (4, 32000, 8), (1, 50257, 32), (9, 128000, 20), (130, 8193, 5),
+                                   (1000, 4096, 3), (891, 4101, 0), (2100, 5001, 32)])
 def test_logprobs_match_oracle(clean, T, V, k, dtype):
     x, tokens = _logits(T, V, dtype, 7 * T + V + k)
     _check(x, tokens, k, _run(x, tokens, k))
@@ -168,9 +170,36 @@ def test_large_magnitudes(clean):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_masks_of_the_lowest_value(clean, dtype):
+    # entries barred by the type's lowest value: beside real logits, alone, and beside -inf
+    x, tokens = _logits(5, 6000, dtype, 12)
+    low = torch.finfo(dtype).min
+    x[0, 100:3000] = low
+    x[1] = low
+    x[2] = low
+    x[2, ::3] = float("-inf")
+    x[3] = float("-inf")
+    x[3, 4321] = low
+    x[4] = 1e30
+    x[4, 7:] = -1e30
+    tokens[:] = torch.tensor([150, 5, 4, 4321, 3])
+    lp, H, lse, tv, ti = _run(x, tokens, 5)
+    assert torch.equal(ti[1:].cpu(), torch.tensor([[0, 1, 2, 3, 4], [1, 2, 4, 5, 7], [4321, 0, 1, 2, 3], [0, 1, 2, 3, 4]],
+                                                  dtype=torch.int32))
+    n = np.array([6000, 4000, 1, 7])
+    assert host(lp)[0] == float(low) and np.all(host(lse)[1:4] == float(low))
+    np.testing.assert_allclose(host(lp)[1:], -np.log(n), rtol=4 * U, atol=0)
+    np.testing.assert_allclose(host(H)[1:], np.log(n), rtol=4 * U, atol=0)
+    np.testing.assert_allclose(host(tv)[1:3], -np.log(n[:2, None]) * np.ones(5), rtol=4 * U, atol=0)
+    assert host(tv)[3, 0] == 0 and np.all(host(tv)[3, 1:] == -np.inf)
+
+
+@gpu
 @pytest.mark.parametrize("kind", ["constant", "falling", "rising", "one_thread", "two_values", "zeros"])
 @pytest.mark.parametrize("V", [255, 9000, 70000])
 def test_ties_and_orders_that_crowd_the_candidates(clean, kind, V):
+    T = 2 if V != 9000 else 900
     x = {"constant": torch.full((2, V), 1.5),
          "falling": -torch.arange(V).float()[None].repeat(2, 1) / 64,
          "rising": torch.arange(V).float()[None].repeat(2, 1) / 64,
@@ -178,7 +207,8 @@ def test_ties_and_orders_that_crowd_the_candidates(clean, kind, V):
          "one_thread": ((torch.arange(V) // 4 % 256) == 3).float()[None].repeat(2, 1) * 4 + torch.linspace(0, 1, V),
          "two_values": (torch.arange(V) % 3 == 1).float()[None].repeat(2, 1),
          "zeros": torch.where(torch.arange(V) % 2 == 0, 0.0, -0.0)[None].repeat(2, 1)}[kind].cuda()
-    tokens = torch.tensor([0, V - 1], dtype=torch.int32, device="cuda")
+    x = x.repeat(T // 2, 1)
+    tokens = torch.tensor([0, V - 1], dtype=torch.int32, device="cuda").repeat(T // 2)
     _check(x, tokens, 32, _run(x, tokens, 32))
 
 
