@@ -387,6 +387,80 @@ quip_status quip_qmatvec(const quip_transform* tf, const uint32_t* packed, int64
                          const float* scale, int bits, const void* x, int x_dtype, int64_t ldx, int64_t B,
                          float* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 
+/* The most adapters of one quip_adapter_* call, and their largest rank. */
+#define QUIP_ADAPTER_MAX_COUNT 1024
+#define QUIP_ADAPTER_MAX_RANK 256
+
+/*
+ * Low-rank adapters beside a shared projection (the quantized layer's
+ * product, quip_qmatvec): each of T tokens names one of `count` adapters of
+ * rank r, or none, and many requests' adapters are applied in one call:
+ *   h_t = down_l x_t,   y_t = base_t + scale_l up_l^T h_t,   l = ids[t];
+ *   a token with ids[t] < 0 has y_t = base_t and h_t = 0.
+ *   x     : device T x n, x_dtype QUIP_F32 or QUIP_BF16, row stride ldx.
+ *   ids   : device T int32; an id >= count sets QUIP_ERR_ARG in the status
+ *           word and counts as none.
+ *   down  : device count x r x n, up: device count x r x m (both with the rank
+ *           outermost within an adapter: up holds the columns of the usual
+ *           m x r factor as rows), w_dtype QUIP_F32 or QUIP_BF16, contiguous.
+ *           Adapters of a smaller rank fill up with zero rows.
+ *   scale : device count fp32, or NULL for 1.
+ *   base  : device T x m of y's type, row stride ldb, or NULL for 0; may be y
+ *           itself (ldb == ldy), else must not overlap it.
+ *   y     : device T x m, y_dtype QUIP_F32 or QUIP_BF16, row stride ldy.
+ *   h     : device T x r fp32, or NULL: kept for quip_adapter_backward.
+ *   plan  : from quip_adapter_plan for these ids, T and count (a model makes
+ *           it once per batch for all its layers), or NULL: the call makes its
+ *           own in ws where it needs one.  A plan of another T or count sets
+ *           QUIP_ERR_ARG in the status word and nothing is written.
+ *   ws    : quip_adapter_workspace_size(..., 0), or NULL with a plan or T <= 64.
+ * Sums are fp32; y is rounded once.  1 <= r <= QUIP_ADAPTER_MAX_RANK,
+ * 1 <= count <= QUIP_ADAPTER_MAX_COUNT, T <= 2^22, n, m <= 2^24; T = 0 does
+ * nothing.  Any alignment and strides; 16-byte aligned rows of bf16 are
+ * fastest.
+ */
+quip_status quip_adapter_apply(const void* x, int x_dtype, int64_t ldx, const int32_t* ids, int64_t T, int64_t n,
+                               int64_t m, const void* down, const void* up, int w_dtype, int64_t count, int64_t r,
+                               const float* scale, const void* base, int64_t ldb, void* y, int y_dtype, int64_t ldy,
+                               float* h, const void* plan, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The gradients of quip_adapter_apply for dy = dloss/dy (T x m, dy_dtype, row
+ * stride lddy):
+ *   dh_t = scale_l up_l dy_t,  dx_t = dx_base_t + down_l^T dh_t  (dx_base_t without an adapter)
+ *   d_down_l (+)= sum_t dh_t x_t^T,  d_up_l (+)= scale_l sum_t h_t dy_t^T
+ * over the tokens t with ids[t] = l, in an order that depends on ids alone
+ * (equal calls give equal bits).  dbase is dy itself; scale is a constant.
+ *   h       : T x r fp32, as quip_adapter_apply wrote it (d_up only).
+ *   dx_base : T x n of x's type, row stride lddb (the shared projection's part
+ *             of dx), or NULL for 0; may be dx itself (lddb == lddx).
+ *   dx      : T x n of x's type, row stride lddx, or NULL.  It must not overlap
+ *             dy, nor x unless d_down is NULL.
+ *   d_down  : count x r x n fp32, or NULL;  d_up: count x r x m fp32, or NULL.
+ *   accumulate : 0 overwrites d_down and d_up (0 for an adapter without
+ *             tokens), 1 adds to them.
+ *   plan    : as in quip_adapter_apply.
+ *   ws      : quip_adapter_workspace_size(..., 1).
+ */
+quip_status quip_adapter_backward(const void* x, int x_dtype, int64_t ldx, const void* dy, int dy_dtype, int64_t lddy,
+                                  const int32_t* ids, int64_t T, int64_t n, int64_t m, const void* down, const void* up,
+                                  int w_dtype, int64_t count, int64_t r, const float* scale, const float* h,
+                                  const void* dx_base, int64_t lddb, void* dx, int64_t lddx, float* d_down, float* d_up,
+                                  int accumulate, const void* plan, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Group a batch's tokens by adapter, on the device: the plan that
+ * quip_adapter_apply and quip_adapter_backward take.  plan: device,
+ * quip_adapter_plan_size bytes, 256-byte aligned; it depends on ids, T and
+ * count alone and can be used until ids change.
+ */
+quip_status quip_adapter_plan_size(int64_t T, int64_t count, size_t* bytes);
+quip_status quip_adapter_plan(const int32_t* ids, int64_t T, int64_t count, void* plan, size_t plan_bytes, void* stream);
+
+/* Workspace of quip_adapter_apply (backward = 0) or quip_adapter_backward (1). */
+quip_status quip_adapter_workspace_size(int64_t T, int64_t n, int64_t m, int64_t r, int64_t count, int backward,
+                                        size_t* bytes);
+
 /* The largest number of alternatives quip_logprobs returns per row. */
 #define QUIP_LOGPROBS_MAX_TOP 32
 

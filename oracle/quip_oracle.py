@@ -74,7 +74,7 @@ __all__ = [
     "run_pipeline", "STREAM_M_SIGNS", "STREAM_N_SIGNS", "STREAM_M_A", "STREAM_M_B",
     "STREAM_N_A", "STREAM_N_B", "STREAM_M_PERM", "STREAM_N_PERM", "random_permutation",
     "diag_order", "greedy_pass", "quantize_layer", "code_slot_bits", "packed_words", "pack_codes",
-    "unpack_codes", "quantized_matvec", "token_logprobs", "token_logprobs_grad",
+    "unpack_codes", "quantized_matvec", "adapter_apply", "adapter_backward", "token_logprobs", "token_logprobs_grad",
 ]
 
 # ----------------------------------------------------------------------------
@@ -603,6 +603,42 @@ def quantized_matvec(codes: np.ndarray, lo: np.ndarray, s: np.ndarray, U: SideTr
     original-domain matrix times each vector."""
     W_hat = incoherence_inverse(dequantize(codes, lo, s), U, V)
     return np.asarray(x, dtype=np.float64) @ W_hat.T
+
+
+# ----------------------------------------------------------------------------
+# Low-rank adapters beside the shared projection
+# ----------------------------------------------------------------------------
+
+
+def adapter_apply(x: np.ndarray, ids: np.ndarray, down: np.ndarray, up: np.ndarray, scale: np.ndarray,
+                  base: np.ndarray) -> Tuple[np.ndarray, np.ndarray]:
+    """(y, h): h_t = down_l x_t and y_t = base_t + scale_l up_l^T h_t for token
+    t's adapter l = ids[t]; y_t = base_t and h_t = 0 where ids[t] < 0.
+    x (T, n), down (count, r, n), up (count, r, m), base (T, m)."""
+    y = np.array(base, dtype=np.float64)
+    h = np.zeros((x.shape[0], down.shape[1]))
+    for t, l in enumerate(ids):
+        if l >= 0:
+            h[t] = np.asarray(down[l], dtype=np.float64) @ x[t]
+            y[t] += scale[l] * (h[t] @ up[l])
+    return y, h
+
+
+def adapter_backward(x: np.ndarray, dy: np.ndarray, ids: np.ndarray, down: np.ndarray, up: np.ndarray,
+                     scale: np.ndarray, h: np.ndarray, dx_base: np.ndarray):
+    """(dx, d_down, d_up, dh) of adapter_apply for dy: dh_t = scale_l up_l dy_t,
+    dx_t = dx_base_t + down_l^T dh_t, d_down_l = sum_t dh_t x_t^T, d_up_l =
+    scale_l sum_t h_t dy_t^T over adapter l's tokens."""
+    dx = np.array(dx_base, dtype=np.float64)
+    d_down, d_up = np.zeros(down.shape), np.zeros(up.shape)
+    dh = np.zeros(h.shape)
+    for t, l in enumerate(ids):
+        if l >= 0:
+            dh[t] = scale[l] * (np.asarray(up[l], dtype=np.float64) @ dy[t])
+            dx[t] += dh[t] @ down[l]
+            d_down[l] += np.outer(dh[t], x[t])
+            d_up[l] += scale[l] * np.outer(h[t], dy[t])
+    return dx, d_down, d_up, dh
 
 
 # ----------------------------------------------------------------------------

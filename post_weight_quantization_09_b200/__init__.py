@@ -10,6 +10,7 @@ inverse transform) with buffers allocated once.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
@@ -24,6 +25,7 @@ __all__ = [
     "quip_incoherence_inverse", "quip_ldl", "quip_ldlq_quantize", "quip_dequantize",
     "quip_nearest_quantize", "quip_diag_order", "quip_permute", "quip_greedy_refine", "METHODS",
     "quip_packed_words", "quip_pack_codes", "quip_qmatvec", "QuantizedLinear",
+    "quip_adapter_plan", "quip_adapter_apply", "quip_adapter_backward", "quip_adapter_workspace_size", "Adapters",
     "quip_logprobs", "quip_logprobs_backward", "TokenScores",
     "quip_workspace_size", "quip_layer_workspace_size", "quip_quantize_layer", "quip_quantize_layer_host",
     "layer_views", "quip_sync_status", "quip_timing_begin", "quip_timing_end", "quip_timing_trace", "LayerQuantizer",
@@ -374,12 +376,23 @@ class QuantizedLinear:
         self.ws = torch.empty(max(quip_workspace_size(L.QUIP_OP_QMATVEC, tf, tf.m, tf.n, max_batch), 256),
                               dtype=torch.uint8, device=codes.device)
 
-    def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None,
+                 adapters: Optional["Adapters"] = None, ids: Optional[torch.Tensor] = None,
+                 h: Optional[torch.Tensor] = None, plan: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """W^ x[b], plus with ``adapters`` the low-rank term of adapter ids[b] of
+        each row (none where ids[b] < 0).  h (B x r fp32) keeps the adapters'
+        hidden vectors for their gradients, plan is the batch's
+        (quip_adapter_plan)."""
         if x.shape[0] > self.max_batch:
             raise ValueError(f"batch {x.shape[0]} > max_batch {self.max_batch}")
+        if (adapters is None) != (ids is None):
+            raise ValueError("adapters and ids go together")
         if out is None:
             out = torch.empty(x.shape[0], self.m, dtype=torch.float32, device=x.device)
         quip_qmatvec(self.tf, self.packed, self.lo, self.scale, self.bits, x, out, self.ws, self.stream)
+        if adapters is not None:
+            quip_adapter_apply(x, ids, adapters.down, adapters.up, adapters.scale, out, base=out, h=h, plan=plan,
+                               stream=self.stream)
         return out
 
     def score(self, x: torch.Tensor, tokens: torch.Tensor, top: int = 0) -> "TokenScores":
@@ -404,6 +417,123 @@ class QuantizedLinear:
                 quip_logprobs(y, tokens[a:b], r.logprob[a:b], r.entropy[a:b], r.lse[a:b],
                               r.top_values[a:b] if top else None, r.top_ids[a:b] if top else None, self.stream)
         return r
+
+
+@dataclass
+class Adapters:
+    """Low-rank adapters of one layer: down (count x r x n) and up (count x r x m)
+    of one type (fp32 or bf16), scale (count fp32, None: 1)."""
+    down: torch.Tensor
+    up: torch.Tensor
+    scale: Optional[torch.Tensor] = None
+
+
+def _scratch(nbytes: int, stream) -> torch.Tensor:
+    """Workspace of the stream that uses it, so that its memory is only handed
+    on behind the call's work."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+# below this many tokens quip_adapter_apply needs neither plan nor workspace
+_ADAPTER_DIRECT = 64
+
+
+@functools.lru_cache(maxsize=256)
+def quip_adapter_workspace_size(T: int, n: int, m: int, r: int, count: int, backward: bool = False) -> int:
+    nb = ctypes.c_size_t()
+    L.check(load().quip_adapter_workspace_size(T, n, m, r, count, int(backward), ctypes.byref(nb)),
+            "quip_adapter_workspace_size")
+    return nb.value
+
+
+@functools.lru_cache(maxsize=256)
+def _adapter_plan_bytes(T: int, count: int) -> int:
+    nb = ctypes.c_size_t()
+    L.check(load().quip_adapter_plan_size(T, count, ctypes.byref(nb)), "quip_adapter_plan_size")
+    return nb.value
+
+
+def quip_adapter_plan(ids: torch.Tensor, count: int, plan: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A batch's tokens grouped by adapter, for quip_adapter_apply and
+    quip_adapter_backward on the same ids (T int32) and number of adapters."""
+    dev = torch.cuda.current_device() if ids.is_cuda else -2
+    T = ids.shape[0]
+    i = _here("ids", ids, _I32, (T,), dev)
+    nb = _adapter_plan_bytes(T, count)
+    if plan is None:
+        plan = _scratch(nb, stream)
+    L.check(load().quip_adapter_plan(i, T, count, plan.data_ptr(), plan.numel(), _raw_stream(stream)),
+            "quip_adapter_plan")
+    return plan
+
+
+def _adapter_factors(down: torch.Tensor, up: torch.Tensor, scale: Optional[torch.Tensor], n: int, m: int, dev: int):
+    count, r = down.shape[0], down.shape[1]
+    return (count, r, _here("down", down, _FLOATS, (count, r, n), dev), _here("up", up, (down.dtype,), (count, r, m), dev),
+            None if scale is None else _here("scale", scale, _F32, (count,), dev))
+
+
+def _adapter_plan_ptr(plan: Optional[torch.Tensor], T: int, count: int, dev: int):
+    if plan is None:
+        return None
+    return _here("plan", plan, (torch.uint8,), (_adapter_plan_bytes(T, count),), dev)
+
+
+def quip_adapter_apply(x: torch.Tensor, ids: torch.Tensor, down: torch.Tensor, up: torch.Tensor,
+                       scale: Optional[torch.Tensor], y: torch.Tensor, base: Optional[torch.Tensor] = None,
+                       h: Optional[torch.Tensor] = None, plan: Optional[torch.Tensor] = None,
+                       ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y[t] = base[t] + scale[l] up[l]^T (down[l] x[t]) with l = ids[t] (just
+    base[t], 0 without one, where ids[t] < 0); h[t] = down[l] x[t] (include/quip.h).
+    base may be y."""
+    (T, n), m = x.shape, y.shape[1]
+    dev = torch.cuda.current_device() if x.is_cuda else -2
+    px = _here("x", x, _FLOATS, (T, n), dev, rows=True)
+    py = _here("y", y, _FLOATS, (T, m), dev, rows=True)
+    count, r, pd, pu, ps = _adapter_factors(down, up, scale, n, m, dev)
+    pb = None if base is None else _here("base", base, (y.dtype,), (T, m), dev, rows=True)
+    if ws is None and plan is None and T > _ADAPTER_DIRECT:
+        ws = _scratch(quip_adapter_workspace_size(T, n, m, r, count), stream)
+    L.check(load().quip_adapter_apply(
+        px, _dtype(x), _row_stride(x), _here("ids", ids, _I32, (T,), dev), T, n, m, pd, pu, _dtype(down), count, r, ps,
+        pb, 0 if base is None else _row_stride(base), py, _dtype(y), _row_stride(y),
+        None if h is None else _here("h", h, _F32, (T, r), dev), _adapter_plan_ptr(plan, T, count, dev),
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _raw_stream(stream)),
+        "quip_adapter_apply")
+
+
+def quip_adapter_backward(x: torch.Tensor, dy: torch.Tensor, ids: torch.Tensor, down: torch.Tensor, up: torch.Tensor,
+                          scale: Optional[torch.Tensor], h: Optional[torch.Tensor], dx: Optional[torch.Tensor] = None,
+                          dx_base: Optional[torch.Tensor] = None, d_down: Optional[torch.Tensor] = None,
+                          d_up: Optional[torch.Tensor] = None, accumulate: bool = False,
+                          plan: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The gradients of quip_adapter_apply for dy = dloss/dy: dx (x's type, on
+    top of dx_base), d_down and d_up (fp32; added to with ``accumulate``);
+    each is computed where it is given."""
+    (T, n), m = x.shape, dy.shape[1]
+    dev = torch.cuda.current_device() if x.is_cuda else -2
+    px = _here("x", x, _FLOATS, (T, n), dev, rows=True)
+    pdy = _here("dy", dy, _FLOATS, (T, m), dev, rows=True)
+    count, r, pd, pu, ps = _adapter_factors(down, up, scale, n, m, dev)
+    if d_up is not None and h is None:
+        raise ValueError("d_up needs h")
+    if dx_base is not None and dx is None:
+        raise ValueError("dx_base without dx")
+    if ws is None:
+        ws = _scratch(quip_adapter_workspace_size(T, n, m, r, count, True), stream)
+    L.check(load().quip_adapter_backward(
+        px, _dtype(x), _row_stride(x), pdy, _dtype(dy), _row_stride(dy), _here("ids", ids, _I32, (T,), dev), T, n, m,
+        pd, pu, _dtype(down), count, r, ps, None if h is None else _here("h", h, _F32, (T, r), dev),
+        None if dx_base is None else _here("dx_base", dx_base, (x.dtype,), (T, n), dev, rows=True),
+        0 if dx_base is None else _row_stride(dx_base),
+        None if dx is None else _here("dx", dx, (x.dtype,), (T, n), dev, rows=True), 0 if dx is None else _row_stride(dx),
+        None if d_down is None else _here("d_down", d_down, _F32, (count, r, n), dev),
+        None if d_up is None else _here("d_up", d_up, _F32, (count, r, m), dev), int(accumulate),
+        _adapter_plan_ptr(plan, T, count, dev), ws.data_ptr(), ws.numel(), _raw_stream(stream)),
+        "quip_adapter_backward")
 
 
 def quip_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], logprob: Optional[torch.Tensor],

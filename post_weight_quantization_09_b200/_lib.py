@@ -17,6 +17,7 @@ QUIP_T_PERMUTE = 0x100
 QUIP_OP_INCOHERENCE_FORWARD, QUIP_OP_INCOHERENCE_INVERSE, QUIP_OP_LDL, QUIP_OP_LDLQ = 0, 1, 2, 3
 QUIP_OP_GREEDY, QUIP_OP_QMATVEC = 4, 5
 QUIP_LOGPROBS_MAX_TOP = 32
+QUIP_ADAPTER_MAX_COUNT, QUIP_ADAPTER_MAX_RANK = 1024, 256
 
 # name -> (restype, argtypes); the list of every symbol include/quip.h declares
 SIGNATURES = {
@@ -53,6 +54,16 @@ SIGNATURES = {
     "quip_pack_codes": (c_int, [c_void_p, c_int64, c_int64, c_int, c_void_p, c_int64, c_void_p]),
     "quip_qmatvec": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int, c_void_p, c_int,
                              c_int64, c_int64, c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
+    "quip_adapter_plan_size": (c_int, [c_int64, c_int64, POINTER(c_size_t)]),
+    "quip_adapter_plan": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_size_t, c_void_p]),
+    "quip_adapter_workspace_size": (c_int, [c_int64, c_int64, c_int64, c_int64, c_int64, c_int, POINTER(c_size_t)]),
+    "quip_adapter_apply": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p,
+                                   c_int, c_int64, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_int, c_int64,
+                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "quip_adapter_backward": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_int, c_int64, c_void_p, c_int64, c_int64,
+                                      c_int64, c_void_p, c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p,
+                                      c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int, c_void_p,
+                                      c_void_p, c_size_t, c_void_p]),
     "quip_logprobs": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
                               c_int, c_void_p, c_void_p, c_void_p]),
     "quip_logprobs_backward": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,

@@ -1,0 +1,532 @@
+// Low-rank adapters beside a shared (quantised) projection: every token of a
+// batch names one of `count` adapters, or none,
+//   h_t = P_l x_t          (P: r x n, "shrink")
+//   y_t = base_t + s_l Q_l^T h_t   (Q: r x m, "expand"),  l = ids_t.
+// Both factors are stored as r rows of the layer's width, so the gradient's
+// products dh_t = s_l up_l dy_t and dx_t = base_t + down_l^T dh_t are the same
+// kernel with P = up, Q = down, and the two weight gradients
+//   d_down_l = sum_t dh_t x_t^T,  d_up_l = s_l sum_t h_t dy_t^T
+// are one kernel for an outer product summed over an adapter's tokens.
+//
+// The arithmetic is 4 T r (n + m) flops forward and backward together with
+// the activations and the factors of the adapters in use to read: at ranks up
+// to 64 the bytes bound it.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+
+namespace quip {
+namespace adapter {
+
+namespace cg = cooperative_groups;
+
+constexpr int MAX_COUNT = QUIP_ADAPTER_MAX_COUNT;
+constexpr int MAX_RANK = QUIP_ADAPTER_MAX_RANK;
+
+// ---------------------------------------------------------------- plan
+// The batch's tokens grouped by adapter (int32 words, device memory):
+//   header  HEAD words
+//   start   count + 2: where adapter l's tokens begin in `order`; entry
+//           `count` is the tokens without an adapter, entry count + 1 is T
+//   order   T: the tokens, by adapter, within one in their own order
+//   tiles   (adapter, first position in order) of up to TILE tokens of one
+//           adapter each, those without an adapter last (adapter `count`)
+//   small   the same for SMALL tokens
+//   chunks  the same for CHUNK tokens, for the sums over an adapter's tokens:
+//           every adapter has one at least; (adapter, first, slot), slot = -1
+//           for an adapter's only chunk, else its place among the partial sums
+//   parts   (first slot, number of slots) per adapter, 0 slots with one chunk
+constexpr int HEAD = 16, TILE = 128, SMALL = 8, CHUNK = 512;
+enum { H_MAGIC, H_T, H_COUNT, H_TILES, H_SMALL, H_CHUNKS, H_BAD };
+constexpr int MAGIC = 0x51AD;
+
+struct PlanView {
+  int32_t *head, *start, *order;
+  int2 *tiles, *small;
+  int4* chunks;
+  int2* parts;
+};
+__host__ __device__ inline int64_t max_tiles(int64_t T, int64_t count, int size) { return T / size + count + 1; }
+// Chunks that belong to adapters of several: fewer than 2 T / CHUNK.
+__host__ __device__ inline int64_t max_slots(int64_t T) { return 2 * (T / CHUNK); }
+__host__ __device__ inline int64_t up4(int64_t v) { return (v + 3) / 4 * 4; }
+__host__ __device__ inline int64_t plan_words(int64_t T, int64_t count) {
+  return HEAD + up4(count + 2) + up4(T) + up4(2 * max_tiles(T, count, TILE)) + up4(2 * max_tiles(T, count, SMALL)) +
+         4 * max_tiles(T, count, CHUNK) + up4(2 * count);
+}
+__host__ __device__ inline PlanView plan_view(void* plan, int64_t T, int64_t count) {
+  int32_t* p = static_cast<int32_t*>(plan);
+  PlanView v;
+  v.head = p;
+  v.start = p + HEAD;
+  v.order = v.start + up4(count + 2);
+  v.tiles = reinterpret_cast<int2*>(v.order + up4(T));
+  v.small = reinterpret_cast<int2*>(reinterpret_cast<int32_t*>(v.tiles) + up4(2 * max_tiles(T, count, TILE)));
+  v.chunks = reinterpret_cast<int4*>(reinterpret_cast<int32_t*>(v.small) + up4(2 * max_tiles(T, count, SMALL)));
+  v.parts = reinterpret_cast<int2*>(v.chunks + max_tiles(T, count, CHUNK));
+  return v;
+}
+
+// One CTA of 32 warps: a stable counting sort of the tokens by adapter, each
+// warp a contiguous share of the tokens with counters of its own (a warp's
+// equal ids are ranked by match.any), then the tables.  Shared memory:
+// 32 x (count + 1) counters.
+constexpr int PLAN_WARPS = 32;
+inline size_t plan_smem(int64_t count) { return (size_t)PLAN_WARPS * (count + 1) * sizeof(int); }
+
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {   // exclusive, 1024 threads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  const int s = warp_sums[lane];
+  int scan = s;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += u;
+  }
+  const int before = __shfl_sync(0xffffffffu, scan - s, warp);
+  total = __shfl_sync(0xffffffffu, scan, 31);
+  __syncthreads();                 // warp_sums may be written again
+  return before + inc - v;
+}
+
+__global__ void __launch_bounds__(PLAN_WARPS * 32)
+    k_adapter_plan(const int32_t* __restrict__ ids, int T, int count, void* plan) {
+  extern __shared__ int counters[];            // [warp][count + 1]
+  __shared__ int warp_sums[32];
+  pdl_wait_then_release();
+  const PlanView pv = plan_view(plan, T, count);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = count + 1;
+  int* mine = counters + warp * nb;
+  for (int i = lane; i < nb; i += 32) mine[i] = 0;
+  __syncwarp();
+  const int per = (T + PLAN_WARPS * 32 - 1) / (PLAN_WARPS * 32) * 32;
+  const int t0 = min(T, warp * per), t1 = min(T, t0 + per);
+  auto bucket = [&](int t, bool report) {
+    int b = ids[t];
+    if (b >= count && report) record_status(QUIP_ERR_ARG);
+    return b < 0 || b >= count ? count : b;
+  };
+  for (int t = t0; t < t1; t += 32) {
+    const int b = t + lane < t1 ? bucket(t + lane, true) : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, b);
+    if (b >= 0 && lane == __ffs(same) - 1) mine[b] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  // per bucket: the warps' counts to offsets within it
+  int total = 0;
+  if (tid < count) {
+    for (int w = 0; w < PLAN_WARPS; ++w) {
+      const int c = counters[w * nb + tid];
+      counters[w * nb + tid] = total;
+      total += c;
+    }
+  }
+  int with, ntile, nsmall, nchunk, nslot;
+  const int first = block_scan(tid < count ? total : 0, warp_sums, with);
+  const int tile0 = block_scan(tid < count ? (total + TILE - 1) / TILE : 0, warp_sums, ntile);
+  const int small0 = block_scan(tid < count ? (total + SMALL - 1) / SMALL : 0, warp_sums, nsmall);
+  const int my_chunks = tid < count ? max(1, (total + CHUNK - 1) / CHUNK) : 0;
+  const int chunk0 = block_scan(my_chunks, warp_sums, nchunk);
+  const int my_slots = my_chunks > 1 ? my_chunks : 0;
+  const int slot0 = block_scan(my_slots, warp_sums, nslot);
+  if (tid < count) {
+    pv.start[tid] = first;
+    pv.parts[tid] = make_int2(slot0, my_slots);
+    for (int w = 0; w < PLAN_WARPS; ++w) counters[w * nb + tid] += first;
+  }
+  if (tid == 0) {
+    int at = with;                             // the tokens without an adapter come last
+    for (int w = 0; w < PLAN_WARPS; ++w) {
+      const int c = counters[w * nb + count];
+      counters[w * nb + count] = at;
+      at += c;
+    }
+    pv.start[count] = with;
+    pv.start[count + 1] = T;
+    pv.head[H_MAGIC] = MAGIC;
+    pv.head[H_T] = T;
+    pv.head[H_COUNT] = count;
+    pv.head[H_TILES] = ntile + (T - with + TILE - 1) / TILE;
+    pv.head[H_SMALL] = nsmall + (T - with + SMALL - 1) / SMALL;
+    pv.head[H_CHUNKS] = nchunk;
+  }
+  __syncthreads();
+  for (int t = t0; t < t1; t += 32) {
+    const int b = t + lane < t1 ? bucket(t + lane, false) : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, b);
+    if (b >= 0) pv.order[mine[b] + __popc(same & ((1u << lane) - 1u))] = t + lane;
+    __syncwarp();
+    if (b >= 0 && lane == __ffs(same) - 1) mine[b] += __popc(same);
+    __syncwarp();
+  }
+  // the tables, a warp per adapter: thread l's numbers go through shared memory
+  __syncthreads();
+  if (tid < count) {
+    counters[tid * 6] = first, counters[tid * 6 + 1] = total, counters[tid * 6 + 2] = tile0;
+    counters[tid * 6 + 3] = small0, counters[tid * 6 + 4] = chunk0, counters[tid * 6 + 5] = my_slots ? slot0 : -1;
+  }
+  __syncthreads();
+  for (int l = warp; l <= count; l += PLAN_WARPS) {
+    const bool none = l == count;
+    const int f = none ? with : counters[l * 6], c = none ? T - with : counters[l * 6 + 1];
+    const int t = none ? ntile : counters[l * 6 + 2], s = none ? nsmall : counters[l * 6 + 3];
+    for (int i = lane; i * TILE < c; i += 32) pv.tiles[t + i] = make_int2(l, f + i * TILE);
+    for (int i = lane; i * SMALL < c; i += 32) pv.small[s + i] = make_int2(l, f + i * SMALL);
+    if (!none) {
+      const int k = counters[l * 6 + 4], slot = counters[l * 6 + 5];
+      for (int i = lane; i == 0 || i * CHUNK < c; i += 32)
+        pv.chunks[k + i] = make_int4(l, f + i * CHUNK, slot < 0 ? -1 : slot + i, 0);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- helpers
+
+// Four consecutive values as fp32; `vec`: one aligned load, else element by
+// element, `left` of them there (the others 0).
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p, bool vec, int left);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p, bool vec, int left) {
+  if (vec && left >= 4) return __ldg(reinterpret_cast<const float4*>(p));
+  return make_float4(left > 0 ? p[0] : 0.f, left > 1 ? p[1] : 0.f, left > 2 ? p[2] : 0.f, left > 3 ? p[3] : 0.f);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p, bool vec, int left) {
+  if (vec && left >= 4) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+  }
+  auto at = [&](int i) { return left > i ? __bfloat162float(p[i]) : 0.f; };
+  return make_float4(at(0), at(1), at(2), at(3));
+}
+// y[0..4) = base[0..4) + v; base may be null or y itself.
+template <typename T>
+__device__ __forceinline__ void put(T* y, float v);
+template <>
+__device__ __forceinline__ void put<float>(float* y, float v) { *y = v; }
+template <>
+__device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
+template <typename T>
+__device__ __forceinline__ void add4(T* y, const T* base, float4 v, bool vec, int left) {
+  float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (vec && left >= 4) {
+    if constexpr (sizeof(T) == 4) {
+      if (base) b = *reinterpret_cast<const float4*>(base);
+      *reinterpret_cast<float4*>(y) = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
+    } else {
+      if (base) {
+        const uint2 u = *reinterpret_cast<const uint2*>(base);
+        b = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                        __uint_as_float(u.y & 0xFFFF0000u));
+      }
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(b.x + v.x, b.y + v.y), hi = __floats2bfloat162_rn(b.z + v.z, b.w + v.w);
+      *reinterpret_cast<uint2*>(y) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+    return;
+  }
+  const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) put(y + i, (base ? to_f32(base[i]) : 0.f) + w[i]);
+}
+
+template <typename TX, typename TW, typename TY>
+struct ApplyArgs {
+  const TX* x;                 // T x n
+  int64_t ldx;
+  const TW *P, *Q;             // count x r x n, count x r x m
+  const float* scale;          // count, or null: 1
+  const TY* base;              // T x m, null: 0; may be y
+  int64_t ldb;
+  TY* y;                       // T x m, null: no expand
+  int64_t ldy;
+  float* h;                    // T x r, or null
+  int T, n, m, r, count;
+  bool h_scaled;               // h gets s_l P_l x_t instead of P_l x_t
+  bool vec_x, vec_p, vec_q, vec_y;
+};
+
+// The plan of a call must be one made for its T and count.
+__device__ __forceinline__ bool plan_ok(const PlanView& pv, int T, int count) {
+  const bool ok = pv.head[H_MAGIC] == MAGIC && pv.head[H_T] == T && pv.head[H_COUNT] == count;
+  if (!ok && threadIdx.x == 0) record_status(QUIP_ERR_ARG);
+  return ok;
+}
+
+// ---------------------------------------------------------------- vectors
+// A few tokens of one adapter per cluster: NTOK = 1 takes token
+// blockIdx / cluster straight from ids (decode; no plan), NTOK = SMALL the
+// plan's small tiles.  The CTAs of a cluster share n, exchange their partial
+// h through distributed shared memory (summed in rank order by each), and
+// share m.  All sums are fp32 on the CUDA cores; any type, rank and alignment.
+constexpr int VT = 256;                        // threads per CTA
+template <int NTOK> __host__ __device__ constexpr int vec_rows() { return NTOK == 1 ? 2 : 4; }   // rows of P per warp task
+template <int NTOK> __host__ __device__ constexpr int vec_cols() { return NTOK == 1 ? 4096 : 1024; }   // of x staged at once
+
+template <int NTOK>
+inline size_t vec_smem(int r) {
+  return sizeof(float) * ((size_t)NTOK * vec_cols<NTOK>() + (size_t)(VT / 32) * NTOK * vec_rows<NTOK>() +
+                          3 * (size_t)NTOK * up4(r) + 16);
+}
+
+template <int NTOK, typename TX, typename TW, typename TY>
+__global__ void __launch_bounds__(VT)
+    k_adapter_vec(const __grid_constant__ ApplyArgs<TX, TW, TY> a, const int32_t* __restrict__ ids, void* plan) {
+  constexpr int R = vec_rows<NTOK>(), COLS = vec_cols<NTOK>();
+  extern __shared__ __align__(16) float sm[];
+  __shared__ int tok[NTOK];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int unit = blockIdx.x / nc;
+  pdl_wait_then_release();
+  int l, cnt = 1;
+  if constexpr (NTOK == 1) {
+    l = ids[unit];
+    if (l >= a.count && rank == 0 && tid == 0) record_status(QUIP_ERR_ARG);
+    if (l < 0 || l >= a.count) l = a.count;
+    if (tid == 0) tok[0] = unit;
+  } else {
+    const PlanView pv = plan_view(plan, a.T, a.count);
+    if (!plan_ok(pv, a.T, a.count) || unit >= pv.head[H_SMALL]) return;    // the whole cluster
+    const int2 tile = pv.small[unit];
+    l = tile.x;
+    cnt = min(NTOK, pv.start[l + 1] - tile.y);
+    if (tid < NTOK) tok[tid] = tid < cnt ? pv.order[tile.y + tid] : -1;
+  }
+  __syncthreads();
+  const int r = a.r, r4 = (int)up4(r);
+  float* xs = sm;                              // [NTOK][COLS]
+  float* parts = xs + NTOK * COLS;             // [warp][R][NTOK] of a warp's rows
+  float* hpart = parts + (VT / 32) * NTOK * R; // [r4][NTOK], read by the cluster
+  float* hs = hpart + NTOK * r4;               // [r4][NTOK], times the scale
+  const int m_per = ((a.m + nc - 1) / nc + 3) / 4 * 4;
+  const int m0 = min(a.m, rank * m_per), m1 = min(a.m, m0 + m_per);
+  if (l == a.count) {                          // no adapter: y = base, h = 0
+    if (rank == 0 && a.h)
+      for (int i = tid; i < cnt * r; i += VT) a.h[(int64_t)tok[i / r] * r + i % r] = 0.f;
+    if (a.y && a.y != a.base)
+      for (int t = 0; t < cnt; ++t) {
+        const int64_t row = tok[t];
+        for (int c = m0 + 4 * tid; c < m1; c += 4 * VT)
+          add4(a.y + row * a.ldy + c, a.base ? a.base + row * a.ldb + c : nullptr, make_float4(0.f, 0.f, 0.f, 0.f),
+               a.vec_y, m1 - c);
+      }
+    return;
+  }
+  const TW* P = a.P + (int64_t)l * r * a.n;
+  const TW* Q = a.Q + (int64_t)l * r * a.m;
+  const float scale = a.scale ? a.scale[l] : 1.f;
+  // ---- shrink: hpart[j][t] = sum over this CTA's columns of P[j][c] x[t][c]
+  const int n_per = ((a.n + nc - 1) / nc + 3) / 4 * 4;
+  const int n0 = min(a.n, rank * n_per), n1 = min(a.n, n0 + n_per);
+  for (int i = tid; i < NTOK * r4; i += VT) hpart[i] = 0.f;
+  const int tasks = (r + R - 1) / R;
+  // few rows: the warps share their columns (1 to 8 of them; 8 is a multiple)
+  const int share = tasks >= VT / 32 ? 1 : (VT / 32) / tasks;
+  for (int c0 = n0; c0 < n1; c0 += COLS) {
+    const int nc4 = (min(COLS, n1 - c0) + 3) / 4;
+    __syncthreads();
+    for (int i = tid; i < NTOK * nc4; i += VT) {
+      const int t = i / nc4, q = i % nc4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (tok[t] >= 0) v = load4(a.x + (int64_t)tok[t] * a.ldx + c0 + 4 * q, a.vec_x, n1 - c0 - 4 * q);
+      reinterpret_cast<float4*>(xs + t * COLS)[q] = v;
+    }
+    __syncthreads();
+    for (int task = warp / share; task < tasks; task += (VT / 32) / share) {
+      const int j0 = task * R;
+      float acc[R][NTOK];
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int t = 0; t < NTOK; ++t) acc[k][t] = 0.f;
+#pragma unroll 4
+        for (int q = lane + 32 * (warp % share); q < nc4; q += 32 * share) {
+          const int left = n1 - c0 - 4 * q;
+          float4 w[R];
+#pragma unroll
+          for (int k = 0; k < R; ++k)
+            w[k] = j0 + k < r ? load4(P + (int64_t)(j0 + k) * a.n + c0 + 4 * q, a.vec_p, left)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int t = 0; t < NTOK; ++t) {
+            const float4 v = reinterpret_cast<const float4*>(xs + t * COLS)[q];
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+              acc[k][t] = fmaf(w[k].x, v.x, acc[k][t]);
+              acc[k][t] = fmaf(w[k].y, v.y, acc[k][t]);
+              acc[k][t] = fmaf(w[k].z, v.z, acc[k][t]);
+              acc[k][t] = fmaf(w[k].w, v.w, acc[k][t]);
+            }
+          }
+        }
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int t = 0; t < NTOK; ++t) acc[k][t] = warp_sum(acc[k][t]);
+      if (share == 1) {
+        if (lane == 0)
+#pragma unroll
+          for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int t = 0; t < NTOK; ++t)
+              if (j0 + k < r) hpart[(j0 + k) * NTOK + t] += acc[k][t];
+      } else if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+          for (int t = 0; t < NTOK; ++t) parts[(warp * R + k) * NTOK + t] = acc[k][t];
+      }
+    }
+    if (share > 1) {                           // one task per warp: add its sharers in order
+      __syncthreads();
+      for (int i = tid; i < tasks * R * NTOK; i += VT) {
+        const int task = i / (R * NTOK), e = i % (R * NTOK);
+        float v = 0.f;
+        for (int s = 0; s < share; ++s) v += parts[(task * share + s) * R * NTOK + e];
+        if (task * R + e / NTOK < r) hpart[task * R * NTOK + e] += v;
+      }
+    }
+  }
+  cluster.sync();
+  for (int i = tid; i < r * NTOK; i += VT) {
+    float v = 0.f;
+    for (int c = 0; c < nc; ++c) v += *cluster.map_shared_rank(hpart + i, c);
+    const int t = i % NTOK;
+    hs[i] = v * scale;
+    if (rank == 0 && a.h && t < cnt) a.h[(int64_t)tok[t] * r + i / NTOK] = a.h_scaled ? v * scale : v;
+  }
+  cluster.sync();                              // everybody has read hpart; hs is there
+  if (!a.y) return;
+  // ---- expand: y[t][c] = base[t][c] + sum_j Q[j][c] hs[j][t]
+  for (int c = m0 + 4 * tid; c < m1; c += 4 * VT) {
+    float4 acc[NTOK];
+#pragma unroll
+    for (int t = 0; t < NTOK; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int j = 0; j < r; ++j) {
+      const float4 w = load4(Q + (int64_t)j * a.m + c, a.vec_q, m1 - c);
+#pragma unroll
+      for (int t = 0; t < NTOK; ++t) {
+        const float v = hs[j * NTOK + t];
+        acc[t].x = fmaf(w.x, v, acc[t].x);
+        acc[t].y = fmaf(w.y, v, acc[t].y);
+        acc[t].z = fmaf(w.z, v, acc[t].z);
+        acc[t].w = fmaf(w.w, v, acc[t].w);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NTOK; ++t)
+      if (t < cnt) {
+        const int64_t row = tok[t];
+        add4(a.y + row * a.ldy + c, a.base ? a.base + row * a.ldb + c : nullptr, acc[t], a.vec_y, m1 - c);
+      }
+  }
+}
+
+// ---------------------------------------------------------------- sums over an adapter's tokens
+// out[l][j][c] (+)= k_l sum_{t of l} u[t][j] x[t][c], u: T x r fp32, k_l = 1 or
+// scale[l].  One CTA per (chunk, 512 columns, 16 rows j): fp32 sums over the
+// chunk's tokens in their order; an adapter's only chunk goes straight to
+// out, the others to their slot of `partial`, which k_adapter_join adds up.
+template <typename TX>
+struct OuterArgs {
+  const TX* x;
+  int64_t ldx;
+  const float* u;
+  const float* scale;
+  float* out;                  // count x r x width
+  float* partial;              // slots x r x width
+  int T, width, r, count, accumulate;
+  bool vec_x;
+};
+constexpr int OT = 128, OROWS = 16;            // threads; rows of u per CTA
+template <typename TX>
+__global__ void __launch_bounds__(OT) k_adapter_outer(const __grid_constant__ OuterArgs<TX> a, void* plan) {
+  __shared__ float us[64][OROWS];
+  __shared__ int tok[64];
+  pdl_wait_then_release();
+  const PlanView pv = plan_view(plan, a.T, a.count);
+  if (!plan_ok(pv, a.T, a.count) || (int)blockIdx.z >= pv.head[H_CHUNKS]) return;
+  const int4 chunk = pv.chunks[blockIdx.z];
+  const int l = chunk.x, first = chunk.y, cnt = max(0, min(CHUNK, pv.start[l + 1] - first));
+  const int c = (blockIdx.x * OT + threadIdx.x) * 4, j0 = blockIdx.y * OROWS, left = a.width - c;
+  float acc[OROWS][4];
+#pragma unroll
+  for (int j = 0; j < OROWS; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+  for (int t0 = 0; t0 < cnt; t0 += 64) {
+    const int nt = min(64, cnt - t0);
+    __syncthreads();
+    if (threadIdx.x < nt) tok[threadIdx.x] = pv.order[first + t0 + threadIdx.x];
+    __syncthreads();
+    for (int i = threadIdx.x; i < nt * OROWS; i += OT) {
+      const int t = i / OROWS, j = i % OROWS;
+      us[t][j] = j0 + j < a.r ? a.u[(int64_t)tok[t] * a.r + j0 + j] : 0.f;
+    }
+    __syncthreads();
+    if (left > 0) {
+#pragma unroll 4
+      for (int t = 0; t < nt; ++t) {
+        const float4 v = load4(a.x + (int64_t)tok[t] * a.ldx + c, a.vec_x, left);
+#pragma unroll
+        for (int j = 0; j < OROWS; ++j) {
+          const float u = us[t][j];
+          acc[j][0] = fmaf(u, v.x, acc[j][0]);
+          acc[j][1] = fmaf(u, v.y, acc[j][1]);
+          acc[j][2] = fmaf(u, v.z, acc[j][2]);
+          acc[j][3] = fmaf(u, v.w, acc[j][3]);
+        }
+      }
+    }
+  }
+  if (left <= 0) return;
+  const float k = a.scale ? a.scale[l] : 1.f;
+  float* out = chunk.z < 0 ? a.out + (int64_t)l * a.r * a.width : a.partial + (int64_t)chunk.z * a.r * a.width;
+  const bool add = chunk.z < 0 && a.accumulate;
+  for (int j = 0; j < OROWS && j0 + j < a.r; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) {
+        float* o = out + (int64_t)(j0 + j) * a.width + c + i;
+        *o = (add ? *o : 0.f) + k * acc[j][i];
+      }
+}
+
+// out[l] (+)= the sum of adapter l's slots, in their order; two outputs.
+__global__ void __launch_bounds__(256)
+    k_adapter_join(float* out0, const float* part0, int64_t size0, float* out1, const float* part1, int64_t size1, int T,
+                   int count, int accumulate, void* plan) {
+  pdl_wait_then_release();
+  const PlanView pv = plan_view(plan, T, count);
+  if (!plan_ok(pv, T, count)) return;
+  const int l = blockIdx.y;
+  const int2 slots = pv.parts[l];
+  if (slots.y == 0) return;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < size0 + size1; i += gridDim.x * 256ll) {
+    const bool one = i >= size0;
+    const int64_t e = one ? i - size0 : i, size = one ? size1 : size0;
+    const float* p = (one ? part1 : part0) + slots.x * size + e;
+    float* o = (one ? out1 : out0) + l * size + e;
+    float v = accumulate ? *o : 0.f;
+    for (int s = 0; s < slots.y; ++s) v += p[s * size];
+    *o = v;
+  }
+}
+
+}  // namespace adapter
+}  // namespace quip

@@ -11,6 +11,7 @@
 #include <mutex>
 #include <vector>
 
+#include "adapter.cuh"
 #include "common.cuh"
 #include "fwht.cuh"
 #include "gemm_simt.cuh"
@@ -201,23 +202,39 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// Launch as clusters of `cluster` CTAs (grid.x a multiple of it).
+// Launch as clusters of `cluster` CTAs (grid.x a multiple of it), with
+// programmatic stream serialization when the kernel waits for it (pdl).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
-                           cudaStream_t st, Args&&... args) {
+                           bool pdl, cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = cluster;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = pdl ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Allow a kernel `bytes` of dynamic shared memory, once per kernel and device
+// (concurrent first calls set it twice).
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kernel)(KArgs...), int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  return e;
 }
 
 int num_sms() {
@@ -1855,6 +1872,250 @@ quip_status quip_qmatvec(const quip_transform* tf, const uint32_t* packed, int64
 
 }  // extern "C"
 
+// ------------------------------------------------------------------ adapters
+namespace {
+namespace ad = adapter;
+
+quip_status adapter_shape(int64_t T, int64_t n, int64_t m, int64_t r, int64_t count) {
+  return T < 0 || n < 1 || m < 1 || r < 1 || count < 1 || T > (int64_t(1) << 22) || n > (1 << 24) || m > (1 << 24) ||
+                 r > QUIP_ADAPTER_MAX_RANK || count > QUIP_ADAPTER_MAX_COUNT
+             ? QUIP_ERR_SHAPE
+             : QUIP_OK;
+}
+bool float_type(int dtype) { return dtype == QUIP_F32 || dtype == QUIP_BF16; }
+size_t type_bytes(int dtype) { return dtype == QUIP_BF16 ? 2 : 4; }
+// Whether four consecutive values from the start of each row are one aligned load.
+bool rows_of_four(const void* p, int64_t ld, size_t size) {
+  return (reinterpret_cast<uintptr_t>(p) % (4 * size)) == 0 && ld % 4 == 0;
+}
+// Whether two row-strided T x cols regions share a byte.
+bool regions_overlap(const void* a, int64_t lda, int64_t cols_a, size_t size_a, const void* b, int64_t ldb,
+                     int64_t cols_b, size_t size_b, int64_t T) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  return pa < pb + ((T - 1) * ldb + cols_b) * size_b && pb < pa + ((T - 1) * lda + cols_a) * size_a;
+}
+
+struct AdapterWs {
+  size_t plan = 0, dh = 0, part_down = 0, part_up = 0, total = 0;   // offsets
+};
+AdapterWs adapter_ws(int64_t T, int64_t n, int64_t m, int64_t r, int64_t count, bool backward) {
+  AdapterWs w;
+  w.total = round256((size_t)ad::plan_words(T, count) * 4);
+  if (backward) {
+    w.dh = w.total;
+    w.total += round256((size_t)T * r * 4);
+    w.part_down = w.total;
+    w.total += round256((size_t)ad::max_slots(T) * r * n * 4);
+    w.part_up = w.total;
+    w.total += round256((size_t)ad::max_slots(T) * r * m * 4);
+  }
+  return w;
+}
+
+cudaError_t adapter_plan(const int32_t* ids, int64_t T, int64_t count, void* plan, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(ad::k_adapter_plan, (int)ad::plan_smem(ad::MAX_COUNT), done);
+  if (e != cudaSuccess) return e;
+  LaunchScope ls("k_adapter_plan", st);
+  return launch_pdl(ad::k_adapter_plan, dim3(1), dim3(ad::PLAN_WARPS * 32), ad::plan_smem(count), st, ids, (int)T,
+                    (int)count, plan);
+}
+
+// Tokens up to which a cluster per token, without a plan, is taken.
+constexpr int64_t kAdapterDirect = 64;
+
+template <int NTOK, typename TX, typename TW, typename TY>
+cudaError_t adapter_vec(const ad::ApplyArgs<TX, TW, TY>& a, const int32_t* ids, void* plan, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  auto* kernel = ad::k_adapter_vec<NTOK, TX, TW, TY>;
+  cudaError_t e = allow_smem(kernel, (int)ad::vec_smem<NTOK>(ad::MAX_RANK), done);
+  if (e != cudaSuccess) return e;
+  // CTAs per cluster: as the SMs are filled and each still has some columns
+  const int64_t units = NTOK == 1 ? a.T : ad::max_tiles(a.T, a.count, NTOK);
+  const int64_t likely = NTOK == 1 ? a.T : (a.T + NTOK - 1) / NTOK;
+  unsigned nc = 1;
+  while (nc < 8 && likely * nc < 4 * (int64_t)num_sms() && std::max(a.n, a.m) >= 256 * (int64_t)nc) nc *= 2;
+  LaunchScope ls("k_adapter_vec", st);
+  return launch_cluster(kernel, (unsigned)(units * nc), ad::VT, ad::vec_smem<NTOK>(a.r), nc, true, st, a, ids, plan);
+}
+
+template <typename TX, typename TW, typename TY>
+cudaError_t adapter_apply(ad::ApplyArgs<TX, TW, TY> a, const int32_t* ids, void* plan, cudaStream_t st) {
+  a.vec_x = rows_of_four(a.x, a.T > 1 ? a.ldx : 4, sizeof(TX));
+  a.vec_p = rows_of_four(a.P, a.n, sizeof(TW));
+  a.vec_q = rows_of_four(a.Q, a.m, sizeof(TW));
+  a.vec_y = rows_of_four(a.y, a.T > 1 ? a.ldy : 4, sizeof(TY)) &&
+            (!a.base || rows_of_four(a.base, a.T > 1 ? a.ldb : 4, sizeof(TY)));
+  return plan ? adapter_vec<ad::SMALL>(a, ids, plan, st) : adapter_vec<1>(a, ids, nullptr, st);
+}
+
+// P, Q: the factors of the direction (down, up forward; up, down for dx).
+struct AdapterCall {
+  const void* x;
+  int64_t ldx;
+  const void *P, *Q;
+  const float* scale;
+  const void* base;
+  int64_t ldb;
+  void* y;
+  int64_t ldy;
+  float* h;
+  int64_t T, n, m, r, count;
+  bool h_scaled;
+};
+template <typename TX, typename TW, typename TY>
+cudaError_t adapter_typed(const AdapterCall& c, const int32_t* ids, void* plan, cudaStream_t st) {
+  return adapter_apply<TX, TW, TY>({static_cast<const TX*>(c.x), c.ldx, static_cast<const TW*>(c.P),
+                                    static_cast<const TW*>(c.Q), c.scale, static_cast<const TY*>(c.base), c.ldb,
+                                    static_cast<TY*>(c.y), c.ldy, c.h, (int)c.T, (int)c.n, (int)c.m, (int)c.r,
+                                    (int)c.count, c.h_scaled, false, false, false, false},
+                                   ids, plan, st);
+}
+cudaError_t adapter_dispatch(int x_dtype, int w_dtype, int y_dtype, const AdapterCall& c, const int32_t* ids, void* plan,
+                             cudaStream_t st) {
+  typedef __nv_bfloat16 B;
+  const int key = (x_dtype == QUIP_BF16) * 4 + (w_dtype == QUIP_BF16) * 2 + (y_dtype == QUIP_BF16);
+  switch (key) {
+    case 0: return adapter_typed<float, float, float>(c, ids, plan, st);
+    case 1: return adapter_typed<float, float, B>(c, ids, plan, st);
+    case 2: return adapter_typed<float, B, float>(c, ids, plan, st);
+    case 3: return adapter_typed<float, B, B>(c, ids, plan, st);
+    case 4: return adapter_typed<B, float, float>(c, ids, plan, st);
+    case 5: return adapter_typed<B, float, B>(c, ids, plan, st);
+    case 6: return adapter_typed<B, B, float>(c, ids, plan, st);
+    default: return adapter_typed<B, B, B>(c, ids, plan, st);
+  }
+}
+
+template <typename TX>
+cudaError_t adapter_outer(const void* x, int64_t ldx, const float* u, const float* scale, float* out, float* partial,
+                          int64_t T, int64_t width, int64_t r, int64_t count, int accumulate, void* plan,
+                          cudaStream_t st) {
+  const ad::OuterArgs<TX> a{static_cast<const TX*>(x), ldx, u, scale, out, partial, (int)T, (int)width, (int)r,
+                            (int)count, accumulate, rows_of_four(x, T > 1 ? ldx : 4, sizeof(TX))};
+  const dim3 grid((unsigned)((width + 4 * ad::OT - 1) / (4 * ad::OT)), (unsigned)((r + ad::OROWS - 1) / ad::OROWS),
+                  (unsigned)ad::max_tiles(T, count, ad::CHUNK));
+  LaunchScope ls("k_adapter_outer", st);
+  return launch_pdl(ad::k_adapter_outer<TX>, grid, dim3(ad::OT), 0, st, a, plan);
+}
+}  // namespace
+
+extern "C" {
+
+quip_status quip_adapter_plan_size(int64_t T, int64_t count, size_t* bytes) {
+  if (!bytes) return QUIP_ERR_ARG;
+  *bytes = 0;
+  quip_status s = adapter_shape(T, 1, 1, 1, count);
+  if (s != QUIP_OK) return s;
+  *bytes = round256((size_t)ad::plan_words(T, count) * 4);
+  return QUIP_OK;
+}
+
+quip_status quip_adapter_plan(const int32_t* ids, int64_t T, int64_t count, void* plan, size_t plan_bytes, void* stream) {
+  size_t need = 0;
+  quip_status s = quip_adapter_plan_size(T, count, &need);
+  if (s != QUIP_OK) return s;
+  if (T > 0 && !ids) return QUIP_ERR_ARG;
+  s = check_ws(plan, plan_bytes, need);
+  if (s != QUIP_OK) return s;
+  QCHECK(adapter_plan(ids, T, count, plan, S(stream)));
+  return QUIP_OK;
+}
+
+quip_status quip_adapter_workspace_size(int64_t T, int64_t n, int64_t m, int64_t r, int64_t count, int backward,
+                                        size_t* bytes) {
+  if (!bytes) return QUIP_ERR_ARG;
+  *bytes = 0;
+  quip_status s = adapter_shape(T, n, m, r, count);
+  if (s != QUIP_OK) return s;
+  *bytes = adapter_ws(T, n, m, r, count, backward != 0).total;
+  return QUIP_OK;
+}
+
+quip_status quip_adapter_apply(const void* x, int x_dtype, int64_t ldx, const int32_t* ids, int64_t T, int64_t n,
+                               int64_t m, const void* down, const void* up, int w_dtype, int64_t count, int64_t r,
+                               const float* scale, const void* base, int64_t ldb, void* y, int y_dtype, int64_t ldy,
+                               float* h, const void* plan, void* ws, size_t ws_bytes, void* stream) {
+  if (!float_type(x_dtype) || !float_type(w_dtype) || !float_type(y_dtype)) return QUIP_ERR_ARG;
+  quip_status s = adapter_shape(T, n, m, r, count);
+  if (s != QUIP_OK) return s;
+  if (ldx < n || ldy < m || (base && ldb < m)) return QUIP_ERR_SHAPE;
+  if (T == 0) return QUIP_OK;
+  if (!x || !ids || !down || !up || !y) return QUIP_ERR_ARG;
+  const size_t ys = type_bytes(y_dtype);
+  if (base == y ? ldb != ldy : base && regions_overlap(base, ldb, m, ys, y, ldy, m, ys, T)) return QUIP_ERR_ARG;
+  if (regions_overlap(x, ldx, n, type_bytes(x_dtype), y, ldy, m, ys, T)) return QUIP_ERR_ARG;
+  cudaStream_t st = S(stream);
+  void* pl = const_cast<void*>(plan);
+  if (!pl && T > kAdapterDirect) {
+    s = check_ws(ws, ws_bytes, adapter_ws(T, n, m, r, count, false).total);
+    if (s != QUIP_OK) return s;
+    pl = ws;
+    QCHECK(adapter_plan(ids, T, count, pl, st));
+  }
+  if (T <= kAdapterDirect) pl = nullptr;
+  const AdapterCall c{x, ldx, down, up, scale, base, ldb, y, ldy, h, T, n, m, r, count, false};
+  QCHECK(adapter_dispatch(x_dtype, w_dtype, y_dtype, c, ids, pl, st));
+  return QUIP_OK;
+}
+
+quip_status quip_adapter_backward(const void* x, int x_dtype, int64_t ldx, const void* dy, int dy_dtype, int64_t lddy,
+                                  const int32_t* ids, int64_t T, int64_t n, int64_t m, const void* down, const void* up,
+                                  int w_dtype, int64_t count, int64_t r, const float* scale, const float* h,
+                                  const void* dx_base, int64_t lddb, void* dx, int64_t lddx, float* d_down, float* d_up,
+                                  int accumulate, const void* plan, void* ws, size_t ws_bytes, void* stream) {
+  if (!float_type(x_dtype) || !float_type(w_dtype) || !float_type(dy_dtype)) return QUIP_ERR_ARG;
+  quip_status s = adapter_shape(T, n, m, r, count);
+  if (s != QUIP_OK) return s;
+  if ((d_down && ldx < n) || lddy < m || (dx && lddx < n) || (dx && dx_base && lddb < n)) return QUIP_ERR_SHAPE;
+  if (!dx && !d_down && !d_up) return QUIP_OK;
+  if (T > 0 && (!ids || !dy || !up || (dx && !down) || (d_down && !x) || (d_up && !h))) return QUIP_ERR_ARG;
+  if (T > 0 && dx) {
+    const size_t xs = type_bytes(x_dtype);
+    if (dx_base == dx ? lddb != lddx : dx_base && regions_overlap(dx_base, lddb, n, xs, dx, lddx, n, xs, T))
+      return QUIP_ERR_ARG;
+    if (regions_overlap(dy, lddy, m, type_bytes(dy_dtype), dx, lddx, n, xs, T)) return QUIP_ERR_ARG;
+    if (d_down && regions_overlap(x, ldx, n, xs, dx, lddx, n, xs, T)) return QUIP_ERR_ARG;
+  }
+  const AdapterWs w = adapter_ws(T, n, m, r, count, true);
+  s = check_ws(ws, ws_bytes, w.total);
+  if (s != QUIP_OK) return s;
+  cudaStream_t st = S(stream);
+  char* w8 = static_cast<char*>(ws);
+  void* pl = const_cast<void*>(plan);
+  if (!pl) {
+    pl = ws;
+    QCHECK(adapter_plan(ids, T, count, pl, st));
+  }
+  float* dh = reinterpret_cast<float*>(w8 + w.dh);
+  float* part_down = reinterpret_cast<float*>(w8 + w.part_down);
+  float* part_up = reinterpret_cast<float*>(w8 + w.part_up);
+  if (T > 0 && (dx || d_down)) {
+    const AdapterCall c{dy, lddy, up, dx ? down : up, scale, dx ? dx_base : nullptr, lddb, dx, lddx, d_down ? dh : nullptr,
+                        T, m, n, r, count, true};
+    QCHECK(adapter_dispatch(dy_dtype, w_dtype, x_dtype, c, ids, T <= kAdapterDirect ? nullptr : pl, st));
+  }
+  if (d_down)
+    QCHECK(x_dtype == QUIP_BF16
+               ? adapter_outer<__nv_bfloat16>(x, ldx, dh, nullptr, d_down, part_down, T, n, r, count, accumulate, pl, st)
+               : adapter_outer<float>(x, ldx, dh, nullptr, d_down, part_down, T, n, r, count, accumulate, pl, st));
+  if (d_up)
+    QCHECK(dy_dtype == QUIP_BF16
+               ? adapter_outer<__nv_bfloat16>(dy, lddy, h, scale, d_up, part_up, T, m, r, count, accumulate, pl, st)
+               : adapter_outer<float>(dy, lddy, h, scale, d_up, part_up, T, m, r, count, accumulate, pl, st));
+  if ((d_down || d_up) && T > ad::CHUNK) {
+    const int64_t s0 = d_down ? r * n : 0, s1 = d_up ? r * m : 0;
+    const unsigned gx = (unsigned)std::min<int64_t>((s0 + s1 + 255) / 256, 4 * num_sms());
+    LaunchScope ls("k_adapter_join", st);
+    QCHECK(launch_pdl(ad::k_adapter_join, dim3(gx, (unsigned)count), dim3(256), 0, st, d_down, part_down, s0, d_up,
+                      part_up, s1, (int)T, (int)count, accumulate, pl));
+  }
+  return QUIP_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ log probabilities
 namespace {
 // CTAs per row: more where the rows leave SMs idle (k_logprobs keeps four
 // CTAs on an SM) and each still gets a few thousand logits.
@@ -1870,7 +2131,7 @@ cudaError_t logprobs_launch(const void* logits, const lp::Args& a, cudaStream_t 
   const unsigned nc = logprobs_cluster(a.T, a.V);
   LaunchScope ls("k_logprobs", st);
   return launch_cluster(a.k > 0 ? lp::k_logprobs<TX, true> : lp::k_logprobs<TX, false>, (unsigned)a.T * nc, lp::NT, 0,
-                        nc, st, x, a);
+                        nc, false, st, x, a);
 }
 
 template <typename TX>
