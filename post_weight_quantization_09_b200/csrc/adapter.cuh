@@ -257,7 +257,7 @@ struct ApplyArgs {
   float* h;                    // T x r, or null
   int T, n, m, r, count;
   bool h_scaled;               // h gets s_l P_l x_t instead of P_l x_t
-  bool vec_x, vec_p, vec_q, vec_y;
+  bool vec_x, vec_p, vec_q, vec_y;   // rows that allow the kernel's vector loads
 };
 
 // The plan of a call must be one made for its T and count.
@@ -436,6 +436,377 @@ __global__ void __launch_bounds__(VT)
         const int64_t row = tok[t];
         add4(a.y + row * a.ldy + c, a.base ? a.base + row * a.ldb + c : nullptr, acc[t], a.vec_y, m1 - c);
       }
+  }
+}
+
+// ---------------------------------------------------------------- tiles on the tensor cores
+// One cluster per tile of up to 128 tokens of one adapter.  Its CTAs share n:
+// each accumulates h[token][j] over its 64-column blocks with tcgen05
+// (M = 128 tokens, N = r, both operands K-major); the partial sums meet
+// through distributed shared memory (each CTA adds up a share of the tokens,
+// in rank order, and hands the sum to all).  Then they share m: per 128
+// columns, D[column][token] = Q^T h (M = 128 columns, N = tokens, K = r, Q
+// MN-major as it lies in memory), so that a lane holds a column and 32 lanes
+// add to 32 neighbouring columns of a token's row of y.
+//
+// Types: a bf16 value is one operand piece, an fp32 value three (split3), and
+// the products of pieces of order 2 and below are formed: fp32 operands keep
+// fp32 accuracy.  h is fed to the second product in pieces too: two for a
+// bf16 output (2^-17 is left, its rounding is 2^-9), three for an fp32 one.
+// The tensor core drops low bits of the running sum at every step, so the
+// blocks of n are dealt out over several accumulators that are added in fp32.
+//
+// Loads go global -> registers (one block ahead) -> shared memory with the
+// 128-byte swizzle: rows are gathered by token, and no operand needs
+// alignment (16-byte loads where all rows allow it).
+constexpr int TT = 256;                        // threads per CTA
+constexpr int TC_COLS = 256;                   // TMEM columns: two CTAs fit an SM (see tc_smem)
+template <typename T> __host__ __device__ constexpr int pieces() { return sizeof(T) == 2 ? 1 : 3; }
+template <typename TY> __host__ __device__ constexpr int h_pieces() { return sizeof(TY) == 2 ? 2 : 3; }
+constexpr int XT_BYTES = TILE * 128;           // one piece of 128 tokens x 64 columns
+
+// Shared memory after alignment: region A holds the two operand stages, then
+// the partial h, then the pieces of h; region B the summed h, then the tiles
+// of Q (two, one with fp32 factors).
+struct TcLayout {
+  int stage, a, b, total;
+};
+template <typename TX, typename TW, typename TY>
+__host__ __device__ inline TcLayout tc_layout(int r16) {
+  TcLayout s;
+  s.stage = pieces<TX>() * XT_BYTES + pieces<TW>() * r16 * 128;
+  const int hf = TILE * (r16 + 4) * 4, hp = h_pieces<TY>() * ((r16 + 63) / 64) * XT_BYTES;
+  s.a = 2 * s.stage;
+  if (hf > s.a) s.a = hf;
+  if (hp > s.a) s.a = hp;
+  s.a = (s.a + 1023) / 1024 * 1024;
+  s.b = (pieces<TW>() == 1 ? 2 : 1) * pieces<TW>() * r16 * 256;
+  if (hf > s.b) s.b = hf;
+  s.total = s.a + s.b + 1024;
+  // at most two CTAs on an SM: they hold 2 x 256 TMEM columns, so no CTA of
+  // a cluster ever waits for TMEM while its peers wait for it
+  if (s.total < 78 * 1024) s.total = 78 * 1024;
+  return s;
+}
+
+// Eight consecutive values in registers.
+template <typename T> struct Eight;
+template <> struct Eight<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool vec, int left) {
+    if (vec && left >= 8) {
+      v = __ldg(reinterpret_cast<const uint4*>(p));
+      return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = 2 * i < left ? __bfloat16_as_ushort(p[2 * i]) : 0u;
+      const uint32_t hi = 2 * i + 1 < left ? __bfloat16_as_ushort(p[2 * i + 1]) : 0u;
+      w[i] = lo | hi << 16;
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void store(uint8_t* at, int) const { *reinterpret_cast<uint4*>(at) = v; }
+};
+// Eight fp32 values as three pieces, `step` bytes apart.
+template <int NP>
+__device__ __forceinline__ void store_pieces(uint8_t* at, int step, const float (&f)[8]) {
+  uint32_t w[3][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __nv_bfloat16 a[3], b[3];
+    split3(f[2 * i], a[0], a[1], a[2]);
+    split3(f[2 * i + 1], b[0], b[1], b[2]);
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+      w[p][i] = (uint32_t)__bfloat16_as_ushort(a[p]) | (uint32_t)__bfloat16_as_ushort(b[p]) << 16;
+  }
+#pragma unroll
+  for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(at + p * step) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+template <> struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p, bool vec, int left) {
+    a = load4(p, vec, left);
+    b = load4(p + 4, vec, left - 4);
+  }
+  __device__ __forceinline__ void store(uint8_t* at, int step) const {
+    const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    store_pieces<3>(at, step, f);
+  }
+};
+
+// The partial h of one CTA reads MMAs' accumulators: how many, and which one
+// takes the small terms of fp32 operands.
+__host__ __device__ constexpr int tc_accs(int r16) { return r16 <= 64 ? 4 : 2; }
+
+template <typename TX, typename TW, typename TY, int RB>
+__global__ void __launch_bounds__(TT, 2)
+    k_adapter_tc(const __grid_constant__ ApplyArgs<TX, TW, TY> a, void* plan) {
+  constexpr int PX = pieces<TX>(), PW = pieces<TW>(), NP = h_pieces<TY>(), QBUF = PW == 1 ? 2 : 1;
+  constexpr bool SPLIT = PX > 1 || PW > 1;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int tok[TILE];
+  __shared__ uint64_t bars[2];
+  __shared__ uint32_t tmem_base;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait_then_release();
+  const PlanView pv = plan_view(plan, a.T, a.count);
+  const int unit = blockIdx.x / nc;
+  if (!plan_ok(pv, a.T, a.count) || unit >= pv.head[H_TILES]) return;      // the whole cluster
+  const int2 tile = pv.tiles[unit];
+  const int l = tile.x, cnt = min(TILE, pv.start[l + 1] - tile.y), r = a.r;
+  if (tid < TILE) tok[tid] = tid < cnt ? pv.order[tile.y + tid] : -1;
+  const int m_per = ((a.m + nc - 1) / nc + TILE - 1) / TILE * TILE;
+  const int m0 = min(a.m, rank * m_per), m1 = min(a.m, m0 + m_per);
+  if (l == a.count) {                          // no adapter: y = base, h = 0
+    __syncthreads();
+    if (rank == 0 && a.h)
+      for (int i = tid; i < cnt * r; i += TT) a.h[(int64_t)tok[i / r] * r + i % r] = 0.f;
+    if (a.y && a.y != a.base)
+      for (int t = warp; t < cnt; t += TT / 32) {
+        const int64_t row = tok[t];
+        for (int c = m0 + 4 * lane; c < m1; c += 128)
+          add4(a.y + row * a.ldy + c, a.base ? a.base + row * a.ldb + c : nullptr, make_float4(0.f, 0.f, 0.f, 0.f),
+               a.vec_y, m1 - c);
+      }
+    return;
+  }
+  const int r16 = (r + 15) / 16 * 16;
+  const TcLayout lay = tc_layout<TX, TW, TY>(r16);
+  uint8_t* A = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* Bm = A + lay.a;
+  if (tid == 0) {
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(&tmem_base, TC_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  bool ok = true;                  // a wait that ran out is the last: what follows it is not stored
+  const TW* P = a.P + (int64_t)l * r * a.n;
+  const TW* Q = a.Q + (int64_t)l * r * a.m;
+
+  // ---- shrink over the 64-column blocks [k0, k1)
+  const int blocks = (a.n + 63) / 64, per = (blocks + nc - 1) / nc;
+  const int k0 = min(blocks, rank * per), k1 = min(blocks, k0 + per);
+  const int accs = tc_accs(r16), mains = SPLIT ? accs - 1 : accs;
+  Eight<TX> xr[TILE * 8 / TT];
+  Eight<TW> pr[RB * 8 / TT];
+  auto load = [&](int k) {
+    const int c = 64 * k + 8 * (tid % 8), left = a.n - c;
+#pragma unroll
+    for (int i = 0; i < TILE * 8 / TT; ++i) {
+      const int row = tid / 8 + i * (TT / 8), t = tok[row];
+      xr[i].zero();
+      if (t >= 0 && left > 0) xr[i].load(a.x + (int64_t)t * a.ldx + c, a.vec_x, left);
+    }
+#pragma unroll
+    for (int i = 0; i < RB * 8 / TT; ++i) {
+      const int row = tid / 8 + i * (TT / 8);
+      pr[i].zero();
+      if (row < r && left > 0) pr[i].load(P + (int64_t)row * a.n + c, a.vec_p, left);
+    }
+  };
+  if (k0 < k1) load(k0);
+  const uint32_t id1 = make_idesc_bf16(TILE, r16, 0, 0);
+  for (int k = k0; k < k1; ++k) {
+    const int i = k - k0, s = i & 1;
+    if (i >= 2) ok = ok && mbar_wait(&bars[s], (uint32_t)(((i >> 1) - 1) & 1));
+    uint8_t* xs = A + s * lay.stage;
+    uint8_t* ps = xs + PX * XT_BYTES;
+    const int c = tid % 8;
+#pragma unroll
+    for (int j = 0; j < TILE * 8 / TT; ++j) {
+      const int row = tid / 8 + j * (TT / 8);
+      xr[j].store(xs + row * 128 + ((c ^ (row & 7)) << 4), XT_BYTES);
+    }
+#pragma unroll
+    for (int j = 0; j < RB * 8 / TT; ++j) {
+      const int row = tid / 8 + j * (TT / 8);
+      if (row < r16) pr[j].store(ps + row * 128 + ((c ^ (row & 7)) << 4), r16 * 128);
+    }
+    if (k + 1 < k1) load(k + 1);
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0 && ok) {
+      const uint32_t xa = smem_u32(xs), pa = smem_u32(ps);
+      bool small = i > 0;                      // the small terms' accumulator holds something
+#pragma unroll
+      for (int px = 0; px < PX; ++px)
+#pragma unroll
+        for (int pw = 0; pw < PW && px + pw <= 2; ++pw) {
+          const bool main = px + pw == 0;
+          const uint32_t d = tmem + (uint32_t)((main ? i % mains : accs - 1) * r16);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16(d, make_sw128_desc(xa + px * XT_BYTES + kk * 32, 16, 1024),
+                       make_sw128_desc(pa + pw * r16 * 128 + kk * 32, 16, 1024), id1,
+                       (main ? i >= mains : small) || kk > 0);
+          if (!main) small = true;
+        }
+      tc_commit(&bars[s]);
+    }
+  }
+  const int n1 = k1 - k0;
+  // phases of each barrier so far, for the waits of the second half
+  int used[2] = {(n1 + 1) / 2, n1 / 2};
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    if (used[s] > 0) ok = ok && mbar_wait(&bars[s], (uint32_t)((used[s] - 1) & 1));
+  __syncthreads();
+  tc_fence_after();
+  // ---- the partial sums of the cluster's CTAs
+  const int pitch = r16 + 4;
+  float* hpart = reinterpret_cast<float*>(A);
+  float* hs = reinterpret_cast<float*>(Bm);
+  if (warp < 4 && 32 * warp < cnt) {
+    const int t = 32 * warp + lane;
+    const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16);
+    for (int j = 0; j < r16; j += 16) {
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = 0.f;
+      for (int q = accs - 1; q >= 0; --q) {    // the small terms first
+        const bool there = SPLIT && q == accs - 1 ? n1 > 0 : q < n1;
+        if (there) {
+          float w[16];
+          tmem_ld16(at + q * r16 + j, w);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] += w[e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<float4*>(hpart + t * pitch + j + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    }
+  }
+  tc_fence_before();
+  cluster.sync();
+  {
+    const int share = (cnt + nc - 1) / nc, t0 = min(cnt, rank * share), t1 = min(cnt, t0 + share), quads = r16 / 4;
+    for (int i = tid; i < (t1 - t0) * quads; i += TT) {
+      const int t = t0 + i / quads, j = 4 * (i % quads);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < nc; ++c) {
+        const float4 w = *reinterpret_cast<const float4*>(cluster.map_shared_rank(hpart, c) + t * pitch + j);
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+      }
+      const float scale = a.scale ? a.scale[l] : 1.f;
+      const float4 sv = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+      if (a.y)
+        for (int c = 0; c < nc; ++c) *reinterpret_cast<float4*>(cluster.map_shared_rank(hs, c) + t * pitch + j) = sv;
+      if (a.h && ok) {
+        const float4 o = a.h_scaled ? sv : v;
+        const float e[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (j + q < r) a.h[(int64_t)tok[t] * r + j + q] = e[q];
+      }
+    }
+  }
+  cluster.sync();                              // hs is complete, hpart is free
+  tc_fence_after();
+  if (a.y && m0 < m1) {
+    // ---- the pieces of scale h, K-major, 64 ranks to a block
+    const int kb = (r16 + 63) / 64;
+    for (int i = tid; i < cnt * (r16 / 8); i += TT) {
+      const int t = i / (r16 / 8), c = i % (r16 / 8);
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = hs[t * pitch + 8 * c + e];
+      store_pieces<NP>(A + (c / 8) * XT_BYTES + t * 128 + (((c % 8) ^ (t & 7)) << 4), kb * XT_BYTES, f);
+    }
+    __syncthreads();                           // hs is free: Q's tiles go there
+    // ---- expand, 128 columns at a time
+    const int n16 = (cnt + 15) / 16 * 16;
+    const uint32_t id2 = make_idesc_bf16(TILE, n16, 1, 0);
+    const int qtile = PW * r16 * 256;
+    Eight<TW> qr[RB * 16 / TT];
+    auto load_q = [&](int c0) {
+      const int c = c0 + 8 * (tid % 16), left = m1 - c;
+#pragma unroll
+      for (int i = 0; i < RB * 16 / TT; ++i) {
+        const int j = tid / 16 + i * (TT / 16);
+        qr[i].zero();
+        if (j < r && left > 0) qr[i].load(Q + (int64_t)j * a.m + c, a.vec_q, left);
+      }
+    };
+    load_q(m0);
+    const int steps = (m1 - m0 + TILE - 1) / TILE;
+    for (int i = 0; i <= steps; ++i) {
+      if (QBUF == 1 && i > 0) ok = ok && mbar_wait(&bars[(i - 1) & 1], (uint32_t)((used[(i - 1) & 1] - 1) & 1));
+      if (i < steps) {
+        uint8_t* qs = Bm + (i % QBUF) * qtile;
+        const int ch = tid % 16;
+#pragma unroll
+        for (int q = 0; q < RB * 16 / TT; ++q) {
+          const int j = tid / 16 + q * (TT / 16);
+          if (j < r16) qr[q].store(qs + (ch / 8) * (r16 * 128) + j * 128 + (((ch % 8) ^ (j & 7)) << 4), r16 * 256);
+        }
+        if (i + 1 < steps) load_q(m0 + (i + 1) * TILE);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0 && ok) {
+          tc_fence_after();
+          const uint32_t qa = smem_u32(qs), ha = smem_u32(A), d = tmem + (uint32_t)((i & 1) * TILE);
+          bool first = true;
+#pragma unroll
+          for (int ph = NP - 1; ph >= 0; --ph)
+#pragma unroll
+            for (int pw = PW - 1; pw >= 0; --pw) {
+              if (ph + pw > 2) continue;
+              for (int k = 0; k < r16 / 16; ++k) {
+                tc_mma_f16(d, make_sw128_desc(qa + pw * r16 * 256 + k * 2048, r16 * 128, 1024),
+                           make_sw128_desc(ha + (ph * kb + k / 4) * XT_BYTES + (k % 4) * 32, 16, 1024), id2, !first);
+                first = false;
+              }
+            }
+          tc_commit(&bars[i & 1]);
+        }
+        ++used[i & 1];
+      }
+      if (i > 0) {                             // y of the columns before, while the tensor core goes on
+        const int b = (i - 1) & 1, c = m0 + (i - 1) * TILE + 32 * (warp % 4) + lane;
+        if (QBUF > 1) {
+          // used[b] already counts step i - 1; step i took the other barrier
+          ok = ok && mbar_wait(&bars[b], (uint32_t)((used[b] - 1) & 1));
+        }
+        tc_fence_after();
+        const uint32_t at = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + (uint32_t)(b * TILE);
+        for (int t0 = 32 * (warp / 4); t0 < cnt; t0 += 64) {
+          float v[32];
+          tmem_ld32(at + t0, v);
+          if (c < m1 && ok) {
+            float o[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = a.base && t0 + e < cnt ? to_f32(a.base[(int64_t)tok[t0 + e] * a.ldb + c]) : 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (t0 + e < cnt) put(a.y + (int64_t)tok[t0 + e] * a.ldy + c, o[e] + v[e]);
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TC_COLS);
   }
 }
 

@@ -1939,13 +1939,52 @@ cudaError_t adapter_vec(const ad::ApplyArgs<TX, TW, TY>& a, const int32_t* ids, 
   return launch_cluster(kernel, (unsigned)(units * nc), ad::VT, ad::vec_smem<NTOK>(a.r), nc, true, st, a, ids, plan);
 }
 
+// Whether eight values from each row's start are 16-byte loads.
+bool rows_of_eight(const void* p, int64_t ld, size_t size) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
+}
+
+template <int RB, typename TX, typename TW, typename TY>
+cudaError_t adapter_tc(const ad::ApplyArgs<TX, TW, TY>& a, void* plan, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  auto* kernel = ad::k_adapter_tc<TX, TW, TY, RB>;
+  cudaError_t e = allow_smem(kernel, ad::tc_layout<TX, TW, TY>(RB).total, done);
+  if (e != cudaSuccess) return e;
+  const int64_t likely = (a.T + ad::TILE - 1) / ad::TILE, wide = (std::max(a.n, a.m) + 127) / 128;
+  unsigned nc = 1;
+  while (nc < 8 && likely * nc < 2 * (int64_t)num_sms() && nc * 2 <= wide) nc *= 2;
+  LaunchScope ls("k_adapter_tc", st);
+  return launch_cluster(kernel, (unsigned)(ad::max_tiles(a.T, a.count, ad::TILE) * nc), ad::TT,
+                        ad::tc_layout<TX, TW, TY>((a.r + 15) / 16 * 16).total, nc, true, st, a, plan);
+}
+
+// The tensor-core tiles serve the types that a layer's products meet (bf16
+// throughout, a bf16 layer with an fp32 side, fp32 activations) up to the
+// rank whose buffers fit; the rest goes to the vector kernel.
+template <typename TX, typename TW, typename TY>
+constexpr int adapter_tc_rank() {
+  constexpr bool f = sizeof(TX) == 4, wf = sizeof(TW) == 4, yf = sizeof(TY) == 4;
+  return wf ? (f && yf ? 64 : 0) : 128;
+}
+
 template <typename TX, typename TW, typename TY>
 cudaError_t adapter_apply(ad::ApplyArgs<TX, TW, TY> a, const int32_t* ids, void* plan, cudaStream_t st) {
-  a.vec_x = rows_of_four(a.x, a.T > 1 ? a.ldx : 4, sizeof(TX));
+  const int64_t ldx = a.T > 1 ? a.ldx : 8, ldy = a.T > 1 ? a.ldy : 8, ldb = a.T > 1 ? a.ldb : 8;
+  a.vec_y = rows_of_four(a.y, ldy, sizeof(TY)) && (!a.base || rows_of_four(a.base, ldb, sizeof(TY)));
+  constexpr int rank = adapter_tc_rank<TX, TW, TY>();
+  if constexpr (rank > 0) {
+    if (plan && a.r <= rank) {
+      a.vec_x = rows_of_eight(a.x, ldx, sizeof(TX));
+      a.vec_p = rows_of_eight(a.P, a.n, sizeof(TW));
+      a.vec_q = rows_of_eight(a.Q, a.m, sizeof(TW));
+      if constexpr (rank > 64)
+        if (a.r > 64) return adapter_tc<128>(a, plan, st);
+      return adapter_tc<64>(a, plan, st);
+    }
+  }
+  a.vec_x = rows_of_four(a.x, ldx, sizeof(TX));
   a.vec_p = rows_of_four(a.P, a.n, sizeof(TW));
   a.vec_q = rows_of_four(a.Q, a.m, sizeof(TW));
-  a.vec_y = rows_of_four(a.y, a.T > 1 ? a.ldy : 4, sizeof(TY)) &&
-            (!a.base || rows_of_four(a.base, a.T > 1 ? a.ldb : 4, sizeof(TY)));
   return plan ? adapter_vec<ad::SMALL>(a, ids, plan, st) : adapter_vec<1>(a, ids, nullptr, st);
 }
 
