@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(TT, 2)
 
 // ---------------------------------------------------------------- sums over an adapter's tokens
 // out[l][j][c] (+)= k_l sum_{t of l} u[t][j] x[t][c], u: T x r fp32, k_l = 1 or
-// scale[l].  One CTA per (chunk, 512 columns, 16 rows j): fp32 sums over the
+// scale[l], for the ranks above 128.  One CTA per (chunk, 512 columns, 16 rows j): fp32 sums over the
 // chunk's tokens in their order; an adapter's only chunk goes straight to
 // out, the others to their slot of `partial`, which k_adapter_join adds up.
 template <typename TX>
@@ -876,6 +876,148 @@ __global__ void __launch_bounds__(OT) k_adapter_outer(const __grid_constant__ Ou
         float* o = out + (int64_t)(j0 + j) * a.width + c + i;
         *o = (add ? *o : 0.f) + k * acc[j][i];
       }
+}
+
+// The same on the tensor cores, 128 columns and all ranks (up to 128) per
+// CTA: D[column][j] = x^T u (M = 128 columns, N = r, K = tokens, x MN-major as
+// its rows lie in memory), 64 tokens at a time.  u is cut into three bf16
+// pieces; the large terms are dealt out over all accumulators but one, which
+// takes the small ones, so few steps meet in each (tc_accs).
+template <typename TX>
+__host__ __device__ inline int outer_smem(int r16) {
+  return 2 * (64 * 256 * pieces<TX>() + 3 * r16 * 128) + 1024;
+}
+template <typename TX, int RB>
+__global__ void __launch_bounds__(TT, 2) k_adapter_outer_tc(const __grid_constant__ OuterArgs<TX> a, void* plan) {
+  constexpr int PX = pieces<TX>(), XB = 64 * 256;        // bytes of one piece of 64 tokens x 128 columns
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int tok[CHUNK];
+  __shared__ uint64_t bars[2];
+  __shared__ uint32_t tmem_base;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  pdl_wait_then_release();
+  const PlanView pv = plan_view(plan, a.T, a.count);
+  if (!plan_ok(pv, a.T, a.count) || (int)blockIdx.y >= pv.head[H_CHUNKS]) return;
+  const int4 chunk = pv.chunks[blockIdx.y];
+  const int l = chunk.x, cnt = max(0, min(CHUNK, pv.start[l + 1] - chunk.y)), r = a.r;
+  const int c0 = blockIdx.x * 128, r16 = (r + 15) / 16 * 16;
+  for (int i = tid; i < CHUNK; i += TT) tok[i] = i < cnt ? pv.order[chunk.y + i] : -1;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int stage = PX * XB + 3 * r16 * 128;
+  if (tid == 0) {
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(&tmem_base, TC_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  bool ok = true;
+  const int accs = tc_accs(r16), mains = accs - 1, steps = (cnt + 63) / 64;
+  Eight<TX> xr[64 * 16 / TT];
+  float ur[RB * 8 / TT][8];
+  auto load = [&](int i) {
+    const int c = c0 + 8 * (tid % 16), left = a.width - c;
+#pragma unroll
+    for (int k = 0; k < 64 * 16 / TT; ++k) {
+      const int t = tok[64 * i + tid / 16 + k * (TT / 16)];
+      xr[k].zero();
+      if (t >= 0 && left > 0) xr[k].load(a.x + (int64_t)t * a.ldx + c, a.vec_x, left);
+    }
+#pragma unroll
+    for (int k = 0; k < RB * 8 / TT; ++k) {
+      const int e = tid + k * TT, j = e % r16, o = e / r16;          // rank j of tokens 8 o ..
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int t = o < 8 ? tok[64 * i + 8 * o + q] : -1;
+        ur[k][q] = t >= 0 && j < r ? __ldg(a.u + (int64_t)t * r + j) : 0.f;
+      }
+    }
+  };
+  if (steps > 0) load(0);
+  const uint32_t idesc = make_idesc_bf16(128, r16, 1, 0);
+  for (int i = 0; i < steps; ++i) {
+    const int s = i & 1;
+    if (i >= 2) ok = ok && mbar_wait(&bars[s], (uint32_t)(((i >> 1) - 1) & 1));
+    uint8_t* xs = sm + s * stage;
+    uint8_t* us = xs + PX * XB;
+    const int ch = tid % 16;
+#pragma unroll
+    for (int k = 0; k < 64 * 16 / TT; ++k) {
+      const int row = tid / 16 + k * (TT / 16);
+      xr[k].store(xs + (ch / 8) * 8192 + row * 128 + (((ch % 8) ^ (row & 7)) << 4), XB);
+    }
+#pragma unroll
+    for (int k = 0; k < RB * 8 / TT; ++k) {
+      const int e = tid + k * TT, j = e % r16, o = e / r16;
+      if (o < 8) store_pieces<3>(us + j * 128 + ((o ^ (j & 7)) << 4), r16 * 128, ur[k]);
+    }
+    if (i + 1 < steps) load(i + 1);
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0 && ok) {
+      const uint32_t xa = smem_u32(xs), ua = smem_u32(us);
+      bool small = i > 0;
+#pragma unroll
+      for (int px = 0; px < PX; ++px)
+#pragma unroll
+        for (int pu = 0; pu < 3 - px; ++pu) {
+          const bool main = px + pu == 0;
+          const uint32_t d = tmem + (uint32_t)((main ? i % mains : accs - 1) * r16);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16(d, make_sw128_desc(xa + px * XB + kk * 2048, 8192, 1024),
+                       make_sw128_desc(ua + pu * r16 * 128 + kk * 32, 16, 1024), idesc,
+                       (main ? i >= mains : small) || kk > 0);
+          if (!main) small = true;
+        }
+      tc_commit(&bars[s]);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int used = (steps + 1 - s) / 2;
+    if (used > 0) ok = ok && mbar_wait(&bars[s], (uint32_t)((used - 1) & 1));
+  }
+  __syncwarp();
+  tc_fence_after();
+  const int c = c0 + tid;
+  if (warp < 4) {
+    const float k = a.scale ? a.scale[l] : 1.f;
+    float* out = chunk.z < 0 ? a.out + (int64_t)l * r * a.width : a.partial + (int64_t)chunk.z * r * a.width;
+    const bool add = chunk.z < 0 && a.accumulate;
+    const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16);
+    for (int j = 0; j < r16; j += 16) {
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = 0.f;
+      for (int q = accs - 1; q >= 0; --q) {    // the small terms first
+        if (q == accs - 1 ? steps > 0 : q < steps) {
+          float w[16];
+          tmem_ld16(at + q * r16 + j, w);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] += w[e];
+        }
+      }
+      if (c < a.width && ok) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (j + e < r) {
+            float* o = out + (int64_t)(j + e) * a.width + c;
+            *o = (add ? *o : 0.f) + k * v[e];
+          }
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TC_COLS);
+  }
 }
 
 // out[l] (+)= the sum of adapter l's slots, in their order; two outputs.

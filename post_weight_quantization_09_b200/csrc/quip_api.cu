@@ -2026,12 +2026,26 @@ cudaError_t adapter_dispatch(int x_dtype, int w_dtype, int y_dtype, const Adapte
   }
 }
 
+template <int RB, typename TX>
+cudaError_t adapter_outer_tc(const ad::OuterArgs<TX>& a, void* plan, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  auto* kernel = ad::k_adapter_outer_tc<TX, RB>;
+  cudaError_t e = allow_smem(kernel, ad::outer_smem<TX>(RB), done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)((a.width + 127) / 128), (unsigned)ad::max_tiles(a.T, a.count, ad::CHUNK));
+  LaunchScope ls("k_adapter_outer_tc", st);
+  return launch_pdl(kernel, grid, dim3(ad::TT), ad::outer_smem<TX>((a.r + 15) / 16 * 16), st, a, plan);
+}
+
 template <typename TX>
 cudaError_t adapter_outer(const void* x, int64_t ldx, const float* u, const float* scale, float* out, float* partial,
                           int64_t T, int64_t width, int64_t r, int64_t count, int accumulate, void* plan,
                           cudaStream_t st) {
-  const ad::OuterArgs<TX> a{static_cast<const TX*>(x), ldx, u, scale, out, partial, (int)T, (int)width, (int)r,
-                            (int)count, accumulate, rows_of_four(x, T > 1 ? ldx : 4, sizeof(TX))};
+  ad::OuterArgs<TX> a{static_cast<const TX*>(x), ldx, u, scale, out, partial, (int)T, (int)width, (int)r,
+                      (int)count, accumulate, rows_of_eight(x, T > 1 ? ldx : 8, sizeof(TX))};
+  if (r <= 64) return adapter_outer_tc<64>(a, plan, st);
+  if (r <= 128) return adapter_outer_tc<128>(a, plan, st);
+  a.vec_x = rows_of_four(x, T > 1 ? ldx : 4, sizeof(TX));
   const dim3 grid((unsigned)((width + 4 * ad::OT - 1) / (4 * ad::OT)), (unsigned)((r + ad::OROWS - 1) / ad::OROWS),
                   (unsigned)ad::max_tiles(T, count, ad::CHUNK));
   LaunchScope ls("k_adapter_outer", st);
