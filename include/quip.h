@@ -413,7 +413,8 @@ quip_status quip_qmatvec(const quip_transform* tf, const uint32_t* packed, int64
  *           it once per batch for all its layers), or NULL: the call makes its
  *           own in ws where it needs one.  A plan of another T or count sets
  *           QUIP_ERR_ARG in the status word and nothing is written.
- *   ws    : quip_adapter_workspace_size(..., 0), or NULL with a plan or T <= 64.
+ *   ws    : quip_adapter_workspace_size(..., 0), or NULL with T <= 64, or with
+ *           both a plan and h.
  * Sums are fp32; y is rounded once.  1 <= r <= QUIP_ADAPTER_MAX_RANK,
  * 1 <= count <= QUIP_ADAPTER_MAX_COUNT, T <= 2^22, n, m <= 2^24; T = 0 does
  * nothing.  Any alignment and strides; 16-byte aligned rows of bf16 are

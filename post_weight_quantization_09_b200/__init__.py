@@ -495,7 +495,7 @@ def quip_adapter_apply(x: torch.Tensor, ids: torch.Tensor, down: torch.Tensor, u
     py = _here("y", y, _FLOATS, (T, m), dev, rows=True)
     count, r, pd, pu, ps = _adapter_factors(down, up, scale, n, m, dev)
     pb = None if base is None else _here("base", base, (y.dtype,), (T, m), dev, rows=True)
-    if ws is None and plan is None and T > _ADAPTER_DIRECT:
+    if ws is None and (plan is None or h is None) and T > _ADAPTER_DIRECT:
         ws = _scratch(quip_adapter_workspace_size(T, n, m, r, count), stream)
     L.check(load().quip_adapter_apply(
         px, _dtype(x), _row_stride(x), _here("ids", ids, _I32, (T,), dev), T, n, m, pd, pu, _dtype(down), count, r, ps,

@@ -440,14 +440,19 @@ __global__ void __launch_bounds__(VT)
 }
 
 // ---------------------------------------------------------------- tiles on the tensor cores
-// One cluster per tile of up to 128 tokens of one adapter.  Its CTAs share n:
-// each accumulates h[token][j] over its 64-column blocks with tcgen05
-// (M = 128 tokens, N = r, both operands K-major); the partial sums meet
-// through distributed shared memory (each CTA adds up a share of the tokens,
-// in rank order, and hands the sum to all).  Then they share m: per 128
-// columns, D[column][token] = Q^T h (M = 128 columns, N = tokens, K = r, Q
-// MN-major as it lies in memory), so that a lane holds a column and 32 lanes
-// add to 32 neighbouring columns of a token's row of y.
+// Tiles of up to 128 tokens of one adapter, in two launches.
+//
+// Shrink: one cluster per tile whose CTAs share n: each accumulates
+// h[token][j] over its 64-column blocks with tcgen05 (M = 128 tokens, N = r,
+// both operands K-major), the partial sums meet through distributed shared
+// memory (each CTA adds up a share of the tokens, in rank order), h goes to
+// memory.
+//
+// Expand: one CTA per tile and run of column blocks: D[token][column] = h Q
+// (M = 128 tokens, N = the block's columns, K = r, Q MN-major as it lies in
+// memory), so a thread holds 128 bytes of one token's row of y, and adds them
+// to the row's base with 16-byte loads and stores. The base of the next block
+// is on its way while this one is multiplied.
 //
 // Types: a bf16 value is one operand piece, an fp32 value three (split3), and
 // the products of pieces of order 2 and below are formed: fp32 operands keep
@@ -456,38 +461,45 @@ __global__ void __launch_bounds__(VT)
 // The tensor core drops low bits of the running sum at every step, so the
 // blocks of n are dealt out over several accumulators that are added in fp32.
 //
-// Loads go global -> registers (one block ahead) -> shared memory with the
-// 128-byte swizzle: rows are gathered by token, and no operand needs
-// alignment (16-byte loads where all rows allow it).
+// Loads are gathered by token into shared memory with the 128-byte swizzle:
+// by cp.async, several blocks ahead, where bf16 rows allow 16-byte copies
+// (CP); else through registers one block ahead, which also cuts fp32 values
+// into pieces and takes any alignment.
 constexpr int TT = 256;                        // threads per CTA
-constexpr int TC_COLS = 256;                   // TMEM columns: two CTAs fit an SM (see tc_smem)
+constexpr int TC_COLS = 256;                   // TMEM columns: two CTAs fit an SM (see shrink_smem)
 template <typename T> __host__ __device__ constexpr int pieces() { return sizeof(T) == 2 ? 1 : 3; }
 template <typename TY> __host__ __device__ constexpr int h_pieces() { return sizeof(TY) == 2 ? 2 : 3; }
 constexpr int XT_BYTES = TILE * 128;           // one piece of 128 tokens x 64 columns
 
-// Shared memory after alignment: region A holds the two operand stages, then
-// the partial h, then the pieces of h; region B the summed h, then the tiles
-// of Q (two, one with fp32 factors).
-struct TcLayout {
-  int stage, a, b, total;
-};
-template <typename TX, typename TW, typename TY>
-__host__ __device__ inline TcLayout tc_layout(int r16) {
-  TcLayout s;
-  s.stage = pieces<TX>() * XT_BYTES + pieces<TW>() * r16 * 128;
-  const int hf = TILE * (r16 + 4) * 4, hp = h_pieces<TY>() * ((r16 + 63) / 64) * XT_BYTES;
-  s.a = 2 * s.stage;
-  if (hf > s.a) s.a = hf;
-  if (hp > s.a) s.a = hp;
-  s.a = (s.a + 1023) / 1024 * 1024;
-  s.b = (pieces<TW>() == 1 ? 2 : 1) * pieces<TW>() * r16 * 256;
-  if (hf > s.b) s.b = hf;
-  s.total = s.a + s.b + 1024;
+template <typename TX, typename TW>
+__host__ __device__ inline int shrink_stage(int r16) { return pieces<TX>() * XT_BYTES + pieces<TW>() * r16 * 128; }
+template <bool CP> __host__ __device__ inline int shrink_stages(int r16) { return !CP ? 2 : r16 <= 64 ? 4 : 3; }
+template <bool CP, typename TX, typename TW>
+__host__ __device__ inline int shrink_smem(int r16) {
+  int s = shrink_stages<CP>(r16) * shrink_stage<TX, TW>(r16);
+  const int hp = TILE * (r16 + 4) * 4;         // the partial h, in the stages' place
+  if (hp > s) s = hp;
+  s += 1024;
   // at most two CTAs on an SM: they hold 2 x 256 TMEM columns, so no CTA of
   // a cluster ever waits for TMEM while its peers wait for it
-  if (s.total < 78 * 1024) s.total = 78 * 1024;
-  return s;
+  return s < 78 * 1024 ? 78 * 1024 : s;
 }
+// Columns of a block of the expand step, its tiles of Q in flight, its buffers.
+template <typename TY> __host__ __device__ constexpr int expand_cols() { return sizeof(TY) == 2 ? 128 : 64; }
+template <bool CP> __host__ __device__ constexpr int expand_ring() { return CP ? 3 : 2; }
+template <typename TW, typename TY>
+__host__ __device__ inline int expand_tile(int r16) { return pieces<TW>() * r16 * 2 * expand_cols<TY>(); }
+template <bool CP, typename TW, typename TY>
+__host__ __device__ inline int expand_smem(int r16) {
+  return h_pieces<TY>() * ((r16 + 63) / 64) * XT_BYTES + expand_ring<CP>() * expand_tile<TW, TY>(r16) + 1024;
+}
+
+__device__ __forceinline__ void cp16(uint8_t* dst, const void* src, bool there) {   // 16 bytes, or zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Eight consecutive values in registers.
 template <typename T> struct Eight;
@@ -539,18 +551,18 @@ template <> struct Eight<float> {
   }
 };
 
-// The partial h of one CTA reads MMAs' accumulators: how many, and which one
-// takes the small terms of fp32 operands.
+// Accumulators of TC_COLS columns in all: the large terms' and, last, the one
+// that takes the small terms of operands in pieces.
 __host__ __device__ constexpr int tc_accs(int r16) { return r16 <= 64 ? 4 : 2; }
 
-template <typename TX, typename TW, typename TY, int RB>
+template <typename TX, typename TW, int RB, bool CP>
 __global__ void __launch_bounds__(TT, 2)
-    k_adapter_tc(const __grid_constant__ ApplyArgs<TX, TW, TY> a, void* plan) {
-  constexpr int PX = pieces<TX>(), PW = pieces<TW>(), NP = h_pieces<TY>(), QBUF = PW == 1 ? 2 : 1;
+    k_adapter_shrink(const __grid_constant__ ApplyArgs<TX, TW, float> a, void* plan) {
+  constexpr int PX = pieces<TX>(), PW = pieces<TW>(), XR = TILE * 8 / TT, PR = RB * 8 / TT;
   constexpr bool SPLIT = PX > 1 || PW > 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int tok[TILE];
-  __shared__ uint64_t bars[2];
+  __shared__ uint64_t bars[4];
   __shared__ uint32_t tmem_base;
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -562,28 +574,15 @@ __global__ void __launch_bounds__(TT, 2)
   const int2 tile = pv.tiles[unit];
   const int l = tile.x, cnt = min(TILE, pv.start[l + 1] - tile.y), r = a.r;
   if (tid < TILE) tok[tid] = tid < cnt ? pv.order[tile.y + tid] : -1;
-  const int m_per = ((a.m + nc - 1) / nc + TILE - 1) / TILE * TILE;
-  const int m0 = min(a.m, rank * m_per), m1 = min(a.m, m0 + m_per);
-  if (l == a.count) {                          // no adapter: y = base, h = 0
+  if (l == a.count) {                          // no adapter: h = 0
     __syncthreads();
-    if (rank == 0 && a.h)
-      for (int i = tid; i < cnt * r; i += TT) a.h[(int64_t)tok[i / r] * r + i % r] = 0.f;
-    if (a.y && a.y != a.base)
-      for (int t = warp; t < cnt; t += TT / 32) {
-        const int64_t row = tok[t];
-        for (int c = m0 + 4 * lane; c < m1; c += 128)
-          add4(a.y + row * a.ldy + c, a.base ? a.base + row * a.ldb + c : nullptr, make_float4(0.f, 0.f, 0.f, 0.f),
-               a.vec_y, m1 - c);
-      }
+    for (int i = rank * TT + tid; i < cnt * r; i += nc * TT) a.h[(int64_t)tok[i / r] * r + i % r] = 0.f;
     return;
   }
-  const int r16 = (r + 15) / 16 * 16;
-  const TcLayout lay = tc_layout<TX, TW, TY>(r16);
-  uint8_t* A = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* Bm = A + lay.a;
+  const int r16 = (r + 15) / 16 * 16, stages = shrink_stages<CP>(r16), stage = shrink_stage<TX, TW>(r16);
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (tid == 0) {
-    mbar_init(&bars[0], 1);
-    mbar_init(&bars[1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars[i], 1);
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&tmem_base, TC_COLS);
@@ -593,81 +592,111 @@ __global__ void __launch_bounds__(TT, 2)
   const uint32_t tmem = tmem_base;
   bool ok = true;                  // a wait that ran out is the last: what follows it is not stored
   const TW* P = a.P + (int64_t)l * r * a.n;
-  const TW* Q = a.Q + (int64_t)l * r * a.m;
 
-  // ---- shrink over the 64-column blocks [k0, k1)
+  // this CTA's 64-column blocks [k0, k1)
   const int blocks = (a.n + 63) / 64, per = (blocks + nc - 1) / nc;
-  const int k0 = min(blocks, rank * per), k1 = min(blocks, k0 + per);
+  const int k0 = min(blocks, rank * per), steps = min(blocks, k0 + per) - k0;
   const int accs = tc_accs(r16), mains = SPLIT ? accs - 1 : accs;
-  Eight<TX> xr[TILE * 8 / TT];
-  Eight<TW> pr[RB * 8 / TT];
-  auto load = [&](int k) {
-    const int c = 64 * k + 8 * (tid % 8), left = a.n - c;
+  const int ch = tid % 8, row0 = tid / 8;      // this thread's 16-byte column and first row of a block
+  auto spot = [&](int row) { return row * 128 + ((ch ^ (row & 7)) << 4); };
+  const uint32_t idesc = make_idesc_bf16(TILE, r16, 0, 0);
+  auto multiply = [&](int i, int s) {          // one thread
+    const uint32_t xa = smem_u32(sm + s * stage), pa = xa + PX * XT_BYTES;
+    bool small = i > 0;                        // the small terms' accumulator holds something
 #pragma unroll
-    for (int i = 0; i < TILE * 8 / TT; ++i) {
-      const int row = tid / 8 + i * (TT / 8), t = tok[row];
-      xr[i].zero();
-      if (t >= 0 && left > 0) xr[i].load(a.x + (int64_t)t * a.ldx + c, a.vec_x, left);
-    }
+    for (int px = 0; px < PX; ++px)
 #pragma unroll
-    for (int i = 0; i < RB * 8 / TT; ++i) {
-      const int row = tid / 8 + i * (TT / 8);
-      pr[i].zero();
-      if (row < r && left > 0) pr[i].load(P + (int64_t)row * a.n + c, a.vec_p, left);
-    }
+      for (int pw = 0; pw < PW && px + pw <= 2; ++pw) {
+        const bool main = px + pw == 0;
+        const uint32_t d = tmem + (uint32_t)((main ? i % mains : accs - 1) * r16);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_f16(d, make_sw128_desc(xa + px * XT_BYTES + kk * 32, 16, 1024),
+                     make_sw128_desc(pa + pw * r16 * 128 + kk * 32, 16, 1024), idesc,
+                     (main ? i >= mains : small) || kk > 0);
+        if (!main) small = true;
+      }
+    tc_commit(&bars[s]);
   };
-  if (k0 < k1) load(k0);
-  const uint32_t id1 = make_idesc_bf16(TILE, r16, 0, 0);
-  for (int k = k0; k < k1; ++k) {
-    const int i = k - k0, s = i & 1;
-    if (i >= 2) ok = ok && mbar_wait(&bars[s], (uint32_t)(((i >> 1) - 1) & 1));
-    uint8_t* xs = A + s * lay.stage;
-    uint8_t* ps = xs + PX * XT_BYTES;
-    const int c = tid % 8;
+  if constexpr (CP) {
+    auto fill = [&](int i) {
+      if (i < steps) {
+        uint8_t* xs = sm + (i % stages) * stage;
+        const int c = 64 * (k0 + i) + 8 * ch;
 #pragma unroll
-    for (int j = 0; j < TILE * 8 / TT; ++j) {
-      const int row = tid / 8 + j * (TT / 8);
-      xr[j].store(xs + row * 128 + ((c ^ (row & 7)) << 4), XT_BYTES);
-    }
-#pragma unroll
-    for (int j = 0; j < RB * 8 / TT; ++j) {
-      const int row = tid / 8 + j * (TT / 8);
-      if (row < r16) pr[j].store(ps + row * 128 + ((c ^ (row & 7)) << 4), r16 * 128);
-    }
-    if (k + 1 < k1) load(k + 1);
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0 && ok) {
-      const uint32_t xa = smem_u32(xs), pa = smem_u32(ps);
-      bool small = i > 0;                      // the small terms' accumulator holds something
-#pragma unroll
-      for (int px = 0; px < PX; ++px)
-#pragma unroll
-        for (int pw = 0; pw < PW && px + pw <= 2; ++pw) {
-          const bool main = px + pw == 0;
-          const uint32_t d = tmem + (uint32_t)((main ? i % mains : accs - 1) * r16);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f16(d, make_sw128_desc(xa + px * XT_BYTES + kk * 32, 16, 1024),
-                       make_sw128_desc(pa + pw * r16 * 128 + kk * 32, 16, 1024), id1,
-                       (main ? i >= mains : small) || kk > 0);
-          if (!main) small = true;
+        for (int j = 0; j < XR; ++j) {
+          const int row = row0 + j * (TT / 8), t = tok[row];
+          // a row past the tile's tokens only feeds its own sums: nothing is loaded
+          if (t >= 0) cp16(xs + spot(row), a.x + (int64_t)t * a.ldx + (c < a.n ? c : 0), c < a.n);
         }
-      tc_commit(&bars[s]);
+#pragma unroll
+        for (int j = 0; j < PR; ++j) {
+          const int row = row0 + j * (TT / 8);
+          const bool there = row < r && c < a.n;
+          if (row < r16) cp16(xs + XT_BYTES + spot(row), P + (there ? (int64_t)row * a.n + c : 0), there);
+        }
+      }
+      cp_commit();
+    };
+    for (int i = 0; i < stages - 1; ++i) fill(i);
+    for (int i = 0; i < steps; ++i) {
+      if (stages == 4) cp_wait<2>();
+      else cp_wait<1>();
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (tid == 0 && ok) multiply(i, i % stages);
+      // the stage of the step before is the next to be filled
+      if (i > 0) ok = ok && mbar_wait(&bars[(i - 1) % stages], (uint32_t)(((i - 1) / stages) & 1));
+      fill(i + stages - 1);
+    }
+    cp_wait<0>();
+    if (steps > 0) ok = ok && mbar_wait(&bars[(steps - 1) % stages], (uint32_t)(((steps - 1) / stages) & 1));
+  } else {
+    Eight<TX> xr[XR];
+    Eight<TW> pr[PR];
+    auto load = [&](int i) {
+      const int c = 64 * (k0 + i) + 8 * ch, left = a.n - c;
+#pragma unroll
+      for (int j = 0; j < XR; ++j) {
+        const int t = tok[row0 + j * (TT / 8)];
+        xr[j].zero();
+        if (t >= 0 && left > 0) xr[j].load(a.x + (int64_t)t * a.ldx + c, a.vec_x, left);
+      }
+#pragma unroll
+      for (int j = 0; j < PR; ++j) {
+        const int row = row0 + j * (TT / 8);
+        pr[j].zero();
+        if (row < r && left > 0) pr[j].load(P + (int64_t)row * a.n + c, a.vec_p, left);
+      }
+    };
+    if (steps > 0) load(0);
+    for (int i = 0; i < steps; ++i) {
+      const int s = i & 1;
+      if (i >= 2) ok = ok && mbar_wait(&bars[s], (uint32_t)(((i >> 1) - 1) & 1));
+      uint8_t* xs = sm + s * stage;
+#pragma unroll
+      for (int j = 0; j < XR; ++j) xr[j].store(xs + spot(row0 + j * (TT / 8)), XT_BYTES);
+#pragma unroll
+      for (int j = 0; j < PR; ++j) {
+        const int row = row0 + j * (TT / 8);
+        if (row < r16) pr[j].store(xs + PX * XT_BYTES + spot(row), r16 * 128);
+      }
+      if (i + 1 < steps) load(i + 1);
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (tid == 0 && ok) multiply(i, s);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int used = (steps + 1 - s) / 2;
+      if (used > 0) ok = ok && mbar_wait(&bars[s], (uint32_t)((used - 1) & 1));
     }
   }
-  const int n1 = k1 - k0;
-  // phases of each barrier so far, for the waits of the second half
-  int used[2] = {(n1 + 1) / 2, n1 / 2};
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-    if (used[s] > 0) ok = ok && mbar_wait(&bars[s], (uint32_t)((used[s] - 1) & 1));
   __syncthreads();
   tc_fence_after();
   // ---- the partial sums of the cluster's CTAs
   const int pitch = r16 + 4;
-  float* hpart = reinterpret_cast<float*>(A);
-  float* hs = reinterpret_cast<float*>(Bm);
+  float* hpart = reinterpret_cast<float*>(sm);
   if (warp < 4 && 32 * warp < cnt) {
     const int t = 32 * warp + lane;
     const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16);
@@ -676,8 +705,7 @@ __global__ void __launch_bounds__(TT, 2)
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = 0.f;
       for (int q = accs - 1; q >= 0; --q) {    // the small terms first
-        const bool there = SPLIT && q == accs - 1 ? n1 > 0 : q < n1;
-        if (there) {
+        if (SPLIT && q == accs - 1 ? steps > 0 : q < steps) {
           float w[16];
           tmem_ld16(at + q * r16 + j, w);
 #pragma unroll
@@ -690,123 +718,266 @@ __global__ void __launch_bounds__(TT, 2)
     }
   }
   tc_fence_before();
-  cluster.sync();
+  if (nc > 1) cluster.sync();
+  else __syncthreads();
   {
     const int share = (cnt + nc - 1) / nc, t0 = min(cnt, rank * share), t1 = min(cnt, t0 + share), quads = r16 / 4;
+    const float scale = a.h_scaled && a.scale ? a.scale[l] : 1.f;
     for (int i = tid; i < (t1 - t0) * quads; i += TT) {
       const int t = t0 + i / quads, j = 4 * (i % quads);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = 0; c < nc; ++c) {
-        const float4 w = *reinterpret_cast<const float4*>(cluster.map_shared_rank(hpart, c) + t * pitch + j);
-        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-      }
-      const float scale = a.scale ? a.scale[l] : 1.f;
-      const float4 sv = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
-      if (a.y)
-        for (int c = 0; c < nc; ++c) *reinterpret_cast<float4*>(cluster.map_shared_rank(hs, c) + t * pitch + j) = sv;
-      if (a.h && ok) {
-        const float4 o = a.h_scaled ? sv : v;
-        const float e[4] = {o.x, o.y, o.z, o.w};
+      float4 w[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < nc) w[c] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(hpart, c) + t * pitch + j);
+      float4 v = w[0];
+#pragma unroll
+      for (int c = 1; c < 8; ++c)
+        if (c < nc) v.x += w[c].x, v.y += w[c].y, v.z += w[c].z, v.w += w[c].w;
+      const float e[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+      if (ok) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (j + q < r) a.h[(int64_t)tok[t] * r + j + q] = e[q];
       }
     }
   }
-  cluster.sync();                              // hs is complete, hpart is free
-  tc_fence_after();
-  if (a.y && m0 < m1) {
-    // ---- the pieces of scale h, K-major, 64 ranks to a block
-    const int kb = (r16 + 63) / 64;
-    for (int i = tid; i < cnt * (r16 / 8); i += TT) {
-      const int t = i / (r16 / 8), c = i % (r16 / 8);
-      float f[8];
+  if (nc > 1) cluster.sync();                  // the others' shared memory is read until here
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TC_COLS);
+  }
+}
+
+// 128 bytes of a row: 8 vectors of 16, or what of them is left of the row
+template <typename TY>
+__device__ __forceinline__ void load_row(uint4 (&u)[8], const TY* p, bool vec, int left) {
+  constexpr int EV = 16 / sizeof(TY);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = hs[t * pitch + 8 * c + e];
-      store_pieces<NP>(A + (c / 8) * XT_BYTES + t * 128 + (((c % 8) ^ (t & 7)) << 4), kb * XT_BYTES, f);
-    }
-    __syncthreads();                           // hs is free: Q's tiles go there
-    // ---- expand, 128 columns at a time
-    const int n16 = (cnt + 15) / 16 * 16;
-    const uint32_t id2 = make_idesc_bf16(TILE, n16, 1, 0);
-    const int qtile = PW * r16 * 256;
-    Eight<TW> qr[RB * 16 / TT];
-    auto load_q = [&](int c0) {
-      const int c = c0 + 8 * (tid % 16), left = m1 - c;
+  for (int i = 0; i < 8; ++i) {
+    u[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (vec && left >= (i + 1) * EV) {
+      u[i] = *reinterpret_cast<const uint4*>(p + i * EV);
+    } else if (left > i * EV) {
+      alignas(16) TY e[EV];
 #pragma unroll
-      for (int i = 0; i < RB * 16 / TT; ++i) {
-        const int j = tid / 16 + i * (TT / 16);
-        qr[i].zero();
-        if (j < r && left > 0) qr[i].load(Q + (int64_t)j * a.m + c, a.vec_q, left);
-      }
-    };
-    load_q(m0);
-    const int steps = (m1 - m0 + TILE - 1) / TILE;
-    for (int i = 0; i <= steps; ++i) {
-      if (QBUF == 1 && i > 0) ok = ok && mbar_wait(&bars[(i - 1) & 1], (uint32_t)((used[(i - 1) & 1] - 1) & 1));
-      if (i < steps) {
-        uint8_t* qs = Bm + (i % QBUF) * qtile;
-        const int ch = tid % 16;
-#pragma unroll
-        for (int q = 0; q < RB * 16 / TT; ++q) {
-          const int j = tid / 16 + q * (TT / 16);
-          if (j < r16) qr[q].store(qs + (ch / 8) * (r16 * 128) + j * 128 + (((ch % 8) ^ (j & 7)) << 4), r16 * 256);
-        }
-        if (i + 1 < steps) load_q(m0 + (i + 1) * TILE);
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0 && ok) {
-          tc_fence_after();
-          const uint32_t qa = smem_u32(qs), ha = smem_u32(A), d = tmem + (uint32_t)((i & 1) * TILE);
-          bool first = true;
-#pragma unroll
-          for (int ph = NP - 1; ph >= 0; --ph)
-#pragma unroll
-            for (int pw = PW - 1; pw >= 0; --pw) {
-              if (ph + pw > 2) continue;
-              for (int k = 0; k < r16 / 16; ++k) {
-                tc_mma_f16(d, make_sw128_desc(qa + pw * r16 * 256 + k * 2048, r16 * 128, 1024),
-                           make_sw128_desc(ha + (ph * kb + k / 4) * XT_BYTES + (k % 4) * 32, 16, 1024), id2, !first);
-                first = false;
-              }
-            }
-          tc_commit(&bars[i & 1]);
-        }
-        ++used[i & 1];
-      }
-      if (i > 0) {                             // y of the columns before, while the tensor core goes on
-        const int b = (i - 1) & 1, c = m0 + (i - 1) * TILE + 32 * (warp % 4) + lane;
-        if (QBUF > 1) {
-          // used[b] already counts step i - 1; step i took the other barrier
-          ok = ok && mbar_wait(&bars[b], (uint32_t)((used[b] - 1) & 1));
-        }
-        tc_fence_after();
-        const uint32_t at = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + (uint32_t)(b * TILE);
-        for (int t0 = 32 * (warp / 4); t0 < cnt; t0 += 64) {
-          float v[32];
-          tmem_ld32(at + t0, v);
-          if (c < m1 && ok) {
-            float o[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[e] = a.base && t0 + e < cnt ? to_f32(a.base[(int64_t)tok[t0 + e] * a.ldb + c]) : 0.f;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (t0 + e < cnt) put(a.y + (int64_t)tok[t0 + e] * a.ldy + c, o[e] + v[e]);
-          }
-          __syncwarp();
-        }
-        tc_fence_before();
-      }
+      for (int k = 0; k < EV; ++k) e[k] = i * EV + k < left ? p[i * EV + k] : TY(0.f);
+      u[i] = *reinterpret_cast<const uint4*>(e);
     }
   }
+}
+template <typename TY>
+__device__ __forceinline__ void store_vec(TY* p, const uint4& u, bool vec, int left) {
+  constexpr int EV = 16 / sizeof(TY);
+  if (vec && left >= EV) {
+    *reinterpret_cast<uint4*>(p) = u;
+  } else {
+    const TY* e = reinterpret_cast<const TY*>(&u);
+#pragma unroll
+    for (int k = 0; k < EV; ++k)
+      if (k < left) p[k] = e[k];
+  }
+}
+// base + v, rounded once
+__device__ __forceinline__ uint4 add_vec(const uint4& b, const float* v, float) {
+  return make_uint4(__float_as_uint(__uint_as_float(b.x) + v[0]), __float_as_uint(__uint_as_float(b.y) + v[1]),
+                    __float_as_uint(__uint_as_float(b.z) + v[2]), __float_as_uint(__uint_as_float(b.w) + v[3]));
+}
+__device__ __forceinline__ uint4 add_vec(const uint4& b, const float* v, __nv_bfloat16) {
+  const uint32_t u[4] = {b.x, b.y, b.z, b.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 s = __floats2bfloat162_rn(__uint_as_float(u[i] << 16) + v[2 * i],
+                                                   __uint_as_float(u[i] & 0xFFFF0000u) + v[2 * i + 1]);
+    o[i] = *reinterpret_cast<const uint32_t*>(&s);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// `per`: column blocks of a CTA.  a.h as the shrink step left it, times the
+// scale already where a.h_scaled.
+template <typename TW, typename TY, int RB, bool CP>
+__global__ void __launch_bounds__(TT, 2)
+    k_adapter_expand(const __grid_constant__ ApplyArgs<float, TW, TY> a, int per, void* plan) {
+  constexpr int PW = pieces<TW>(), NP = h_pieces<TY>(), CB = expand_cols<TY>(), RING = expand_ring<CP>();
+  constexpr int CH = CB / 8, QROWS = TT / CH, QR = RB / QROWS, EV = 16 / (int)sizeof(TY);
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int tok[TILE];
+  __shared__ uint64_t bars[2];
+  __shared__ uint32_t tmem_base;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = a.r;
+  // The launch before released this one after its own wait: all but h is there.
+  const PlanView pv = plan_view(plan, a.T, a.count);
+  const bool mine = plan_ok(pv, a.T, a.count) && (int)blockIdx.y < pv.head[H_TILES];
+  const int2 tile = mine ? pv.tiles[blockIdx.y] : make_int2(0, 0);
+  const int l = tile.x, cnt = mine ? min(TILE, pv.start[l + 1] - tile.y) : 0;
+  const int blocks = (a.m + CB - 1) / CB, b0 = blockIdx.x * per, steps = min(blocks, b0 + per) - b0;
+  const int token = 32 * (warp % 4) + lane;    // this thread's row of a tile, and its columns of a block
+  const int col = (warp / 4) * (CB / 2);
+  const bool have = token < cnt;
+  const int64_t row = have ? pv.order[tile.y + token] : 0;
+  if (tid < TILE) tok[tid] = tid < cnt ? pv.order[tile.y + tid] : -1;
+  if (!mine || l == a.count) {
+    pdl_wait_then_release();
+    if (mine && a.y != a.base)                 // no adapter: y = base
+      for (int i = 0; i < steps; ++i) {
+        const int c = (b0 + i) * CB + col;
+        uint4 u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (have && a.base) load_row(u, a.base + row * a.ldb + c, a.vec_y, a.m - c);
+        if (have)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) store_vec(a.y + row * a.ldy + c + k * EV, u[k], a.vec_y, a.m - c - k * EV);
+      }
+    return;
+  }
+  const int r16 = (r + 15) / 16 * 16, kb = (r16 + 63) / 64, qtile = expand_tile<TW, TY>(r16);
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qs = sm + NP * kb * XT_BYTES;
+  const TW* Q = a.Q + (int64_t)l * r * a.m;
+  const int ch = tid % CH, j0 = tid / CH;      // this thread's 16-byte column and first row of a tile of Q
+  // MN-major: 64-column boxes of r16 rows x 128 bytes
+  auto spot = [&](int j) { return (ch / 8) * (r16 * 128) + j * 128 + (((ch % 8) ^ (j & 7)) << 4); };
+  auto fill = [&](int i) {
+    if (i < steps) {
+      const int c = (b0 + i) * CB + 8 * ch;
+#pragma unroll
+      for (int q = 0; q < QR; ++q) {
+        const int j = j0 + q * QROWS;
+        const bool there = j < r && c < a.m;
+        if (j < r16) cp16(qs + (i % RING) * qtile + spot(j), Q + (there ? (int64_t)j * a.m + c : 0), there);
+      }
+    }
+    cp_commit();
+  };
+  Eight<TW> qr[CP ? 1 : QR];
+  auto load_q = [&](int i) {
+    const int c = (b0 + i) * CB + 8 * ch, left = a.m - c;
+#pragma unroll
+    for (int q = 0; q < (CP ? 0 : QR); ++q) {
+      const int j = j0 + q * QROWS;
+      qr[q].zero();
+      if (j < r && left > 0) qr[q].load(Q + (int64_t)j * a.m + c, a.vec_q, left);
+    }
+  };
+  if constexpr (CP) {
+    fill(0);
+    fill(1);
+  } else {
+    load_q(0);
+  }
+  uint4 base[8];
+  auto load_base = [&](int i) {
+    const int c = (b0 + i) * CB + col;
+    if (have && a.base) {
+      load_row(base, a.base + row * a.ldb + c, a.vec_y, a.m - c);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) base[k] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  load_base(0);
+  if (tid == 0) {
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(&tmem_base, 2 * CB);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  bool ok = true;
+  pdl_wait_then_release();
+  // ---- the pieces of scale h, K-major, 64 ranks to a block
+  {
+    const float scale = a.scale && !a.h_scaled ? a.scale[l] : 1.f;
+    const int eights = r16 / 8;
+    for (int i = tid; i < cnt * eights; i += TT) {
+      const int t = i / eights, c = i % eights;
+      const float* h = a.h + (int64_t)tok[t] * r + 8 * c;
+      float f[8];
+      if (r % 4 == 0 && (reinterpret_cast<uintptr_t>(a.h) & 15) == 0) {
+        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 u = 8 * c < r ? *reinterpret_cast<const float4*>(h) : z;
+        const float4 w = 8 * c + 4 < r ? *reinterpret_cast<const float4*>(h + 4) : z;
+        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = w.x, f[5] = w.y, f[6] = w.z, f[7] = w.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = 8 * c + e < r ? h[e] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] *= scale;
+      store_pieces<NP>(sm + (c / 8) * XT_BYTES + t * 128 + (((c % 8) ^ (t & 7)) << 4), kb * XT_BYTES, f);
+    }
+  }
+  const uint32_t idesc = make_idesc_bf16(TILE, CB, 0, 1);
+  for (int i = 0; i <= steps; ++i) {
+    if (i < steps) {
+      uint8_t* q = qs + (i % RING) * qtile;
+      if constexpr (CP) {
+        cp_wait<1>();
+      } else {
+#pragma unroll
+        for (int k = 0; k < QR; ++k) {
+          const int j = j0 + k * QROWS;
+          if (j < r16) qr[k].store(q + spot(j), r16 * 2 * CB);
+        }
+        if (i + 1 < steps) load_q(i + 1);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncthreads();
+      if (tid == 0 && ok) {
+        tc_fence_after();
+        const uint32_t qa = smem_u32(q), ha = smem_u32(sm), d = tmem + (uint32_t)((i & 1) * CB);
+        bool first = true;
+#pragma unroll
+        for (int ph = NP - 1; ph >= 0; --ph)   // the small terms first
+#pragma unroll
+          for (int pw = PW - 1; pw >= 0; --pw) {
+            if (ph + pw > 2) continue;
+            for (int k = 0; k < r16 / 16; ++k) {
+              tc_mma_f16(d, make_sw128_desc(ha + (ph * kb + k / 4) * XT_BYTES + (k % 4) * 32, 16, 1024),
+                         make_sw128_desc(qa + pw * r16 * 2 * CB + k * 2048, r16 * 128, 1024), idesc, !first);
+              first = false;
+            }
+          }
+        tc_commit(&bars[i & 1]);
+      }
+    }
+    if (i > 0) {                               // y of the block before, while the tensor core goes on
+      const int b = (i - 1) & 1, c = (b0 + i - 1) * CB + col, left = a.m - c;
+      ok = ok && mbar_wait(&bars[b], (uint32_t)(((i - 1) >> 1) & 1));
+      tc_fence_after();
+      const uint32_t at = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + (uint32_t)(b * CB + col);
+      if (32 * (warp % 4) < cnt) {
+#pragma unroll
+        for (int g = 0; g < CB / 64; ++g) {
+          float v[32];
+          tmem_ld32(at + 32 * g, v);
+          if (have && ok)
+#pragma unroll
+            for (int k = 0; k < 32 / EV; ++k) {
+              const int e = g * (32 / EV) + k;
+              store_vec(a.y + row * a.ldy + c + e * EV, add_vec(base[e], v + k * EV, TY()), a.vec_y, left - e * EV);
+            }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+    }
+    if constexpr (CP) fill(i + 2);             // into the tile that step i - 1 has read
+    if (i > 0 && i < steps) load_base(i);
+  }
+  if constexpr (CP) cp_wait<0>();
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, TC_COLS);
+    tmem_dealloc(tmem, 2 * CB);
   }
 }
 

@@ -1896,14 +1896,13 @@ bool regions_overlap(const void* a, int64_t lda, int64_t cols_a, size_t size_a, 
 }
 
 struct AdapterWs {
-  size_t plan = 0, dh = 0, part_down = 0, part_up = 0, total = 0;   // offsets
+  size_t plan = 0, h = 0, part_down = 0, part_up = 0, total = 0;   // offsets
 };
 AdapterWs adapter_ws(int64_t T, int64_t n, int64_t m, int64_t r, int64_t count, bool backward) {
   AdapterWs w;
-  w.total = round256((size_t)ad::plan_words(T, count) * 4);
+  w.h = w.total = round256((size_t)ad::plan_words(T, count) * 4);
+  w.total += round256((size_t)T * r * 4);
   if (backward) {
-    w.dh = w.total;
-    w.total += round256((size_t)T * r * 4);
     w.part_down = w.total;
     w.total += round256((size_t)ad::max_slots(T) * r * n * 4);
     w.part_up = w.total;
@@ -1944,18 +1943,53 @@ bool rows_of_eight(const void* p, int64_t ld, size_t size) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
 }
 
+template <int RB, bool CP, typename TX, typename TW>
+cudaError_t adapter_shrink(const ad::ApplyArgs<TX, TW, float>& a, void* plan, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  auto* kernel = ad::k_adapter_shrink<TX, TW, RB, CP>;
+  cudaError_t e = allow_smem(kernel, std::max(ad::shrink_smem<CP, TX, TW>(RB), ad::shrink_smem<CP, TX, TW>(64)), done);
+  if (e != cudaSuccess) return e;
+  // CTAs per cluster: as many as fill two per SM, each with a few blocks
+  const int64_t likely = (a.T + ad::TILE - 1) / ad::TILE, blocks = (a.n + 63) / 64;
+  unsigned nc = 1;
+  while (nc < 8 && likely * nc < 2 * (int64_t)num_sms() && nc * 2 <= blocks) nc *= 2;
+  LaunchScope ls("k_adapter_shrink", st);
+  return launch_cluster(kernel, (unsigned)(ad::max_tiles(a.T, a.count, ad::TILE) * nc), ad::TT,
+                        ad::shrink_smem<CP, TX, TW>((a.r + 15) / 16 * 16), nc, true, st, a, plan);
+}
+
+template <int RB, bool CP, typename TW, typename TY>
+cudaError_t adapter_expand(const ad::ApplyArgs<float, TW, TY>& a, void* plan, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  auto* kernel = ad::k_adapter_expand<TW, TY, RB, CP>;
+  cudaError_t e = allow_smem(kernel, ad::expand_smem<CP, TW, TY>(RB), done);
+  if (e != cudaSuccess) return e;
+  // column blocks per CTA: about six CTAs per SM in all, so that the last
+  // ones to run are short, and at most 16 blocks to a CTA's start
+  const int64_t tiles = (a.T + ad::TILE - 1) / ad::TILE, blocks = (a.m + ad::expand_cols<TY>() - 1) / ad::expand_cols<TY>();
+  const int per = (int)std::min<int64_t>(16, std::max<int64_t>(1, tiles * blocks / (6 * num_sms())));
+  const dim3 grid((unsigned)((blocks + per - 1) / per), (unsigned)ad::max_tiles(a.T, a.count, ad::TILE));
+  LaunchScope ls("k_adapter_expand", st);
+  return launch_pdl(kernel, grid, dim3(ad::TT), ad::expand_smem<CP, TW, TY>((a.r + 15) / 16 * 16), st, a, per, plan);
+}
+
 template <int RB, typename TX, typename TW, typename TY>
 cudaError_t adapter_tc(const ad::ApplyArgs<TX, TW, TY>& a, void* plan, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  auto* kernel = ad::k_adapter_tc<TX, TW, TY, RB>;
-  cudaError_t e = allow_smem(kernel, ad::tc_layout<TX, TW, TY>(RB).total, done);
-  if (e != cudaSuccess) return e;
-  const int64_t likely = (a.T + ad::TILE - 1) / ad::TILE, wide = (std::max(a.n, a.m) + 127) / 128;
-  unsigned nc = 1;
-  while (nc < 8 && likely * nc < 2 * (int64_t)num_sms() && nc * 2 <= wide) nc *= 2;
-  LaunchScope ls("k_adapter_tc", st);
-  return launch_cluster(kernel, (unsigned)(ad::max_tiles(a.T, a.count, ad::TILE) * nc), ad::TT,
-                        ad::tc_layout<TX, TW, TY>((a.r + 15) / 16 * 16).total, nc, true, st, a, plan);
+  const bool vec_y = rows_of_eight(a.y, a.T > 1 ? a.ldy : 8, sizeof(TY)) &&
+                     (!a.base || rows_of_eight(a.base, a.T > 1 ? a.ldb : 8, sizeof(TY)));
+  const ad::ApplyArgs<TX, TW, float> s{a.x, a.ldx, a.P, nullptr, a.scale, nullptr, 0, nullptr, 0, a.h, a.T, a.n, a.m,
+                                       a.r, a.count, a.h_scaled, a.vec_x, a.vec_p, false, false};
+  const ad::ApplyArgs<float, TW, TY> x{nullptr, 0, nullptr, a.Q, a.scale, a.base, a.ldb, a.y, a.ldy, a.h, a.T, a.n, a.m,
+                                       a.r, a.count, a.h_scaled, false, false, a.vec_q, vec_y};
+  constexpr bool bf = sizeof(TX) == 2 && sizeof(TW) == 2;
+  cudaError_t e;
+  if constexpr (bf) e = a.vec_x && a.vec_p ? adapter_shrink<RB, true>(s, plan, st) : adapter_shrink<RB, false>(s, plan, st);
+  else e = adapter_shrink<RB, false>(s, plan, st);
+  if (e != cudaSuccess || !a.y) return e;
+  if constexpr (sizeof(TW) == 2)
+    return a.vec_q ? adapter_expand<RB, true>(x, plan, st) : adapter_expand<RB, false>(x, plan, st);
+  else
+    return adapter_expand<RB, false>(x, plan, st);
 }
 
 // The tensor-core tiles serve the types that a layer's products meet (bf16
@@ -1973,7 +2007,7 @@ cudaError_t adapter_apply(ad::ApplyArgs<TX, TW, TY> a, const int32_t* ids, void*
   a.vec_y = rows_of_four(a.y, ldy, sizeof(TY)) && (!a.base || rows_of_four(a.base, ldb, sizeof(TY)));
   constexpr int rank = adapter_tc_rank<TX, TW, TY>();
   if constexpr (rank > 0) {
-    if (plan && a.r <= rank) {
+    if (plan && a.r <= rank) {                 // a.h is there: quip_adapter_apply sees to it
       a.vec_x = rows_of_eight(a.x, ldx, sizeof(TX));
       a.vec_p = rows_of_eight(a.P, a.n, sizeof(TW));
       a.vec_q = rows_of_eight(a.Q, a.m, sizeof(TW));
@@ -2099,14 +2133,20 @@ quip_status quip_adapter_apply(const void* x, int x_dtype, int64_t ldx, const in
   if (base == y ? ldb != ldy : base && regions_overlap(base, ldb, m, ys, y, ldy, m, ys, T)) return QUIP_ERR_ARG;
   if (regions_overlap(x, ldx, n, type_bytes(x_dtype), y, ldy, m, ys, T)) return QUIP_ERR_ARG;
   cudaStream_t st = S(stream);
-  void* pl = const_cast<void*>(plan);
-  if (!pl && T > kAdapterDirect) {
-    s = check_ws(ws, ws_bytes, adapter_ws(T, n, m, r, count, false).total);
-    if (s != QUIP_OK) return s;
-    pl = ws;
-    QCHECK(adapter_plan(ids, T, count, pl, st));
+  void* pl = nullptr;
+  if (T > kAdapterDirect) {
+    const AdapterWs w = adapter_ws(T, n, m, r, count, false);
+    pl = const_cast<void*>(plan);
+    if (!pl || !h) {
+      s = check_ws(ws, ws_bytes, w.total);
+      if (s != QUIP_OK) return s;
+    }
+    if (!h) h = reinterpret_cast<float*>(static_cast<char*>(ws) + w.h);
+    if (!pl) {
+      pl = ws;
+      QCHECK(adapter_plan(ids, T, count, pl, st));
+    }
   }
-  if (T <= kAdapterDirect) pl = nullptr;
   const AdapterCall c{x, ldx, down, up, scale, base, ldb, y, ldy, h, T, n, m, r, count, false};
   QCHECK(adapter_dispatch(x_dtype, w_dtype, y_dtype, c, ids, pl, st));
   return QUIP_OK;
@@ -2140,11 +2180,11 @@ quip_status quip_adapter_backward(const void* x, int x_dtype, int64_t ldx, const
     pl = ws;
     QCHECK(adapter_plan(ids, T, count, pl, st));
   }
-  float* dh = reinterpret_cast<float*>(w8 + w.dh);
+  float* dh = reinterpret_cast<float*>(w8 + w.h);
   float* part_down = reinterpret_cast<float*>(w8 + w.part_down);
   float* part_up = reinterpret_cast<float*>(w8 + w.part_up);
   if (T > 0 && (dx || d_down)) {
-    const AdapterCall c{dy, lddy, up, dx ? down : up, scale, dx ? dx_base : nullptr, lddb, dx, lddx, d_down ? dh : nullptr,
+    const AdapterCall c{dy, lddy, up, dx ? down : up, scale, dx ? dx_base : nullptr, lddb, dx, lddx, dh,
                         T, m, n, r, count, true};
     QCHECK(adapter_dispatch(dy_dtype, w_dtype, x_dtype, c, ids, T <= kAdapterDirect ? nullptr : pl, st));
   }
