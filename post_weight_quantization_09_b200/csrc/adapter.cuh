@@ -450,9 +450,10 @@ __global__ void __launch_bounds__(VT)
 //
 // Expand: one CTA per tile and run of column blocks: D[token][column] = h Q
 // (M = 128 tokens, N = the block's columns, K = r, Q MN-major as it lies in
-// memory), so a thread holds 128 bytes of one token's row of y, and adds them
-// to the row's base with 16-byte loads and stores. The base of the next block
-// is on its way while this one is multiplied.
+// memory).  A TMEM lane is a token; each warp turns 32 tokens x 32 columns
+// through shared memory, so that neighbouring lanes read the base and write y
+// in whole 64- or 128-byte pieces of a row.  The base of the next block is on
+// its way while this one is multiplied.
 //
 // Types: a bf16 value is one operand piece, an fp32 value three (split3), and
 // the products of pieces of order 2 and below are formed: fp32 operands keep
@@ -484,14 +485,14 @@ __host__ __device__ inline int shrink_smem(int r16) {
   // a cluster ever waits for TMEM while its peers wait for it
   return s < 78 * 1024 ? 78 * 1024 : s;
 }
-// Columns of a block of the expand step, its tiles of Q in flight, its buffers.
+// Columns of a block of the expand step, its buffers.
 template <typename TY> __host__ __device__ constexpr int expand_cols() { return sizeof(TY) == 2 ? 128 : 64; }
-template <bool CP> __host__ __device__ constexpr int expand_ring() { return CP ? 3 : 2; }
+constexpr int RING = 2, TURN_BYTES = 32 * 128;  // of each warp
 template <typename TW, typename TY>
 __host__ __device__ inline int expand_tile(int r16) { return pieces<TW>() * r16 * 2 * expand_cols<TY>(); }
-template <bool CP, typename TW, typename TY>
+template <typename TW, typename TY>
 __host__ __device__ inline int expand_smem(int r16) {
-  return h_pieces<TY>() * ((r16 + 63) / 64) * XT_BYTES + expand_ring<CP>() * expand_tile<TW, TY>(r16) + 1024;
+  return h_pieces<TY>() * ((r16 + 63) / 64) * XT_BYTES + RING * expand_tile<TW, TY>(r16) + TT / 32 * TURN_BYTES + 1024;
 }
 
 __device__ __forceinline__ void cp16(uint8_t* dst, const void* src, bool there) {   // 16 bytes, or zeros
@@ -748,22 +749,15 @@ __global__ void __launch_bounds__(TT, 2)
   }
 }
 
-// 128 bytes of a row: 8 vectors of 16, or what of them is left of the row
+// 16 bytes of a row, or what of them is left of it
 template <typename TY>
-__device__ __forceinline__ void load_row(uint4 (&u)[8], const TY* p, bool vec, int left) {
+__device__ __forceinline__ uint4 load_vec(const TY* p, bool vec, int left) {
   constexpr int EV = 16 / sizeof(TY);
+  if (vec && left >= EV) return *reinterpret_cast<const uint4*>(p);
+  alignas(16) TY e[EV];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    u[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (vec && left >= (i + 1) * EV) {
-      u[i] = *reinterpret_cast<const uint4*>(p + i * EV);
-    } else if (left > i * EV) {
-      alignas(16) TY e[EV];
-#pragma unroll
-      for (int k = 0; k < EV; ++k) e[k] = i * EV + k < left ? p[i * EV + k] : TY(0.f);
-      u[i] = *reinterpret_cast<const uint4*>(e);
-    }
-  }
+  for (int k = 0; k < EV; ++k) e[k] = k < left ? p[k] : TY(0.f);
+  return *reinterpret_cast<const uint4*>(e);
 }
 template <typename TY>
 __device__ __forceinline__ void store_vec(TY* p, const uint4& u, bool vec, int left) {
@@ -799,8 +793,9 @@ __device__ __forceinline__ uint4 add_vec(const uint4& b, const float* v, __nv_bf
 template <typename TW, typename TY, int RB, bool CP>
 __global__ void __launch_bounds__(TT, 2)
     k_adapter_expand(const __grid_constant__ ApplyArgs<float, TW, TY> a, int per, void* plan) {
-  constexpr int PW = pieces<TW>(), NP = h_pieces<TY>(), CB = expand_cols<TY>(), RING = expand_ring<CP>();
+  constexpr int PW = pieces<TW>(), NP = h_pieces<TY>(), CB = expand_cols<TY>();
   constexpr int CH = CB / 8, QROWS = TT / CH, QR = RB / QROWS, EV = 16 / (int)sizeof(TY);
+  constexpr int LANES = 32 / EV, ROWS = 32 / LANES;       // lanes on 32 columns of a row; rows at once
   extern __shared__ uint8_t smem_raw[];
   __shared__ int tok[TILE];
   __shared__ uint64_t bars[2];
@@ -812,29 +807,40 @@ __global__ void __launch_bounds__(TT, 2)
   const int2 tile = mine ? pv.tiles[blockIdx.y] : make_int2(0, 0);
   const int l = tile.x, cnt = mine ? min(TILE, pv.start[l + 1] - tile.y) : 0;
   const int blocks = (a.m + CB - 1) / CB, b0 = blockIdx.x * per, steps = min(blocks, b0 + per) - b0;
-  const int token = 32 * (warp % 4) + lane;    // this thread's row of a tile, and its columns of a block
-  const int col = (warp / 4) * (CB / 2);
-  const bool have = token < cnt;
-  const int64_t row = have ? pv.order[tile.y + token] : 0;
+  // this warp's 32 tokens of a tile and CB / 2 columns of a block; of these
+  // vector v of the lane is 16 bytes of 32 columns (v / LANES) of row
+  // (v % LANES) ROWS + lane / LANES
+  const int token0 = 32 * (warp % 4), col = (warp / 4) * (CB / 2);
+  auto vrow = [&](int v) { return token0 + (v % LANES) * ROWS + lane / LANES; };
+  auto vcol = [&](int v) { return col + v / LANES * 32 + lane % LANES * EV; };
   if (tid < TILE) tok[tid] = tid < cnt ? pv.order[tile.y + tid] : -1;
+  __syncthreads();
+  uint4 base[8];
+  auto load_base = [&](int i) {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const int t = vrow(v), c = (b0 + i) * CB + vcol(v);
+      base[v] = make_uint4(0u, 0u, 0u, 0u);
+      if (t < cnt && a.base) base[v] = load_vec(a.base + (int64_t)tok[t] * a.ldb + c, a.vec_y, a.m - c);
+    }
+  };
   if (!mine || l == a.count) {
     pdl_wait_then_release();
     if (mine && a.y != a.base)                 // no adapter: y = base
       for (int i = 0; i < steps; ++i) {
-        const int c = (b0 + i) * CB + col;
-        uint4 u[8];
+        load_base(i);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (have && a.base) load_row(u, a.base + row * a.ldb + c, a.vec_y, a.m - c);
-        if (have)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) store_vec(a.y + row * a.ldy + c + k * EV, u[k], a.vec_y, a.m - c - k * EV);
+        for (int v = 0; v < 8; ++v) {
+          const int t = vrow(v), c = (b0 + i) * CB + vcol(v);
+          if (t < cnt) store_vec(a.y + (int64_t)tok[t] * a.ldy + c, base[v], a.vec_y, a.m - c);
+        }
       }
     return;
   }
   const int r16 = (r + 15) / 16 * 16, kb = (r16 + 63) / 64, qtile = expand_tile<TW, TY>(r16);
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qs = sm + NP * kb * XT_BYTES;
+  float4* turn = reinterpret_cast<float4*>(qs + RING * qtile + warp * TURN_BYTES);
   const TW* Q = a.Q + (int64_t)l * r * a.m;
   const int ch = tid % CH, j0 = tid / CH;      // this thread's 16-byte column and first row of a tile of Q
   // MN-major: 64-column boxes of r16 rows x 128 bytes
@@ -863,20 +869,9 @@ __global__ void __launch_bounds__(TT, 2)
   };
   if constexpr (CP) {
     fill(0);
-    fill(1);
   } else {
     load_q(0);
   }
-  uint4 base[8];
-  auto load_base = [&](int i) {
-    const int c = (b0 + i) * CB + col;
-    if (have && a.base) {
-      load_row(base, a.base + row * a.ldb + c, a.vec_y, a.m - c);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) base[k] = make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
   load_base(0);
   if (tid == 0) {
     mbar_init(&bars[0], 1);
@@ -917,7 +912,7 @@ __global__ void __launch_bounds__(TT, 2)
     if (i < steps) {
       uint8_t* q = qs + (i % RING) * qtile;
       if constexpr (CP) {
-        cp_wait<1>();
+        cp_wait<0>();
       } else {
 #pragma unroll
         for (int k = 0; k < QR; ++k) {
@@ -947,28 +942,39 @@ __global__ void __launch_bounds__(TT, 2)
         tc_commit(&bars[i & 1]);
       }
     }
+    if (i > 0) ok = ok && mbar_wait(&bars[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1));
+    if constexpr (CP) fill(i + 1);             // into the tile that step i - 1 has read
     if (i > 0) {                               // y of the block before, while the tensor core goes on
-      const int b = (i - 1) & 1, c = (b0 + i - 1) * CB + col, left = a.m - c;
-      ok = ok && mbar_wait(&bars[b], (uint32_t)(((i - 1) >> 1) & 1));
       tc_fence_after();
-      const uint32_t at = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + (uint32_t)(b * CB + col);
-      if (32 * (warp % 4) < cnt) {
+      const uint32_t at = tmem + ((uint32_t)token0 << 16) + (uint32_t)(((i - 1) & 1) * CB + col);
+      if (token0 < cnt) {
 #pragma unroll
         for (int g = 0; g < CB / 64; ++g) {
           float v[32];
           tmem_ld32(at + 32 * g, v);
-          if (have && ok)
+          // row `lane`, 16-byte pieces swizzled by the row
 #pragma unroll
-            for (int k = 0; k < 32 / EV; ++k) {
-              const int e = g * (32 / EV) + k;
-              store_vec(a.y + row * a.ldy + c + e * EV, add_vec(base[e], v + k * EV, TY()), a.vec_y, left - e * EV);
+          for (int k = 0; k < 8; ++k)
+            turn[lane * 8 + (k ^ (lane & 7))] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < LANES; ++k) {
+            const int e = g * LANES + k, t = vrow(e), c = (b0 + i - 1) * CB + vcol(e);
+            const int tr = t - token0, piece = lane % LANES * (EV / 4);
+            float d[EV];
+#pragma unroll
+            for (int p = 0; p < EV / 4; ++p) {
+              const float4 f = turn[tr * 8 + ((piece + p) ^ (tr & 7))];
+              d[4 * p] = f.x, d[4 * p + 1] = f.y, d[4 * p + 2] = f.z, d[4 * p + 3] = f.w;
             }
+            if (t < cnt && ok)
+              store_vec(a.y + (int64_t)tok[t] * a.ldy + c, add_vec(base[e], d, TY()), a.vec_y, a.m - c);
+          }
           __syncwarp();
         }
       }
       tc_fence_before();
     }
-    if constexpr (CP) fill(i + 2);             // into the tile that step i - 1 has read
     if (i > 0 && i < steps) load_base(i);
   }
   if constexpr (CP) cp_wait<0>();

@@ -1962,7 +1962,7 @@ template <int RB, bool CP, typename TW, typename TY>
 cudaError_t adapter_expand(const ad::ApplyArgs<float, TW, TY>& a, void* plan, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   auto* kernel = ad::k_adapter_expand<TW, TY, RB, CP>;
-  cudaError_t e = allow_smem(kernel, ad::expand_smem<CP, TW, TY>(RB), done);
+  cudaError_t e = allow_smem(kernel, ad::expand_smem<TW, TY>(RB), done);
   if (e != cudaSuccess) return e;
   // column blocks per CTA: about six CTAs per SM in all, so that the last
   // ones to run are short, and at most 16 blocks to a CTA's start
@@ -1970,7 +1970,7 @@ cudaError_t adapter_expand(const ad::ApplyArgs<float, TW, TY>& a, void* plan, cu
   const int per = (int)std::min<int64_t>(16, std::max<int64_t>(1, tiles * blocks / (6 * num_sms())));
   const dim3 grid((unsigned)((blocks + per - 1) / per), (unsigned)ad::max_tiles(a.T, a.count, ad::TILE));
   LaunchScope ls("k_adapter_expand", st);
-  return launch_pdl(kernel, grid, dim3(ad::TT), ad::expand_smem<CP, TW, TY>((a.r + 15) / 16 * 16), st, a, per, plan);
+  return launch_pdl(kernel, grid, dim3(ad::TT), ad::expand_smem<TW, TY>((a.r + 15) / 16 * 16), st, a, per, plan);
 }
 
 template <int RB, typename TX, typename TW, typename TY>
