@@ -35,10 +35,11 @@ constexpr int MAX_RANK = QUIP_ADAPTER_MAX_RANK;
 //           adapter each, those without an adapter last (adapter `count`)
 //   small   the same for SMALL tokens
 //   chunks  the same for CHUNK tokens, for the sums over an adapter's tokens:
-//           every adapter has one at least; (adapter, first, slot), slot = -1
-//           for an adapter's only chunk, else its place among the partial sums
+//           every adapter has one at least; (adapter, first, slot, sub), slot =
+//           -1 for an adapter's only chunk, else its place among the partial
+//           sums; sub: the number of its first SUB tokens among all runs of SUB
 //   parts   (first slot, number of slots) per adapter, 0 slots with one chunk
-constexpr int HEAD = 16, TILE = 128, SMALL = 8, CHUNK = 512;
+constexpr int HEAD = 16, TILE = 128, SMALL = 8, CHUNK = 512, SUB = 64;
 enum { H_MAGIC, H_T, H_COUNT, H_TILES, H_SMALL, H_CHUNKS, H_BAD };
 constexpr int MAGIC = 0x51AD;
 
@@ -72,37 +73,45 @@ __host__ __device__ inline PlanView plan_view(void* plan, int64_t T, int64_t cou
 // One CTA of 32 warps: a stable counting sort of the tokens by adapter, each
 // warp a contiguous share of the tokens with counters of its own (a warp's
 // equal ids are ranked by match.any), then the tables.  Shared memory:
-// 32 x (count + 1) counters.
+// 32 x (count + 1) counters (later 7 numbers per adapter).
 constexpr int PLAN_WARPS = 32;
 inline size_t plan_smem(int64_t count) { return (size_t)PLAN_WARPS * (count + 1) * sizeof(int); }
 
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {   // exclusive, 1024 threads
+// Exclusive sums of N numbers over 1024 threads, and their totals.
+template <int N>
+__device__ __forceinline__ void block_scan(int (&v)[N], int (&total)[N], int (*warp_sums)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+  int inc[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
+  for (int k = 0; k < N; ++k) {
+    inc[k] = v[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc[k], o);
+      if (lane >= o) inc[k] += u;
+    }
+    if (lane == 31) warp_sums[warp][k] = inc[k];
   }
-  if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  const int s = warp_sums[lane];
-  int scan = s;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += u;
+  for (int k = 0; k < N; ++k) {
+    const int s = warp_sums[lane][k];
+    int scan = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += u;
+    }
+    total[k] = __shfl_sync(0xffffffffu, scan, 31);
+    v[k] = __shfl_sync(0xffffffffu, scan - s, warp) + inc[k] - v[k];
   }
-  const int before = __shfl_sync(0xffffffffu, scan - s, warp);
-  total = __shfl_sync(0xffffffffu, scan, 31);
-  __syncthreads();                 // warp_sums may be written again
-  return before + inc - v;
 }
 
 __global__ void __launch_bounds__(PLAN_WARPS * 32)
     k_adapter_plan(const int32_t* __restrict__ ids, int T, int count, void* plan) {
   extern __shared__ int counters[];            // [warp][count + 1]
-  __shared__ int warp_sums[32];
+  enum { FIRST, TILES, SMALLS, CHUNKS, SLOTS, SUBS, SCANS };
+  __shared__ int warp_sums[32][SCANS];
   pdl_wait_then_release();
   const PlanView pv = plan_view(plan, T, count);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = count + 1;
@@ -124,26 +133,28 @@ __global__ void __launch_bounds__(PLAN_WARPS * 32)
   }
   __syncthreads();
   // per bucket: the warps' counts to offsets within it
-  int total = 0;
+  int total = 0, counts[PLAN_WARPS];
   if (tid < count) {
-    for (int w = 0; w < PLAN_WARPS; ++w) {
-      const int c = counters[w * nb + tid];
-      counters[w * nb + tid] = total;
-      total += c;
-    }
+#pragma unroll
+    for (int w = 0; w < PLAN_WARPS; ++w) counts[w] = counters[w * nb + tid];
+#pragma unroll
+    for (int w = 0; w < PLAN_WARPS; ++w) total += counts[w];
   }
-  int with, ntile, nsmall, nchunk, nslot;
-  const int first = block_scan(tid < count ? total : 0, warp_sums, with);
-  const int tile0 = block_scan(tid < count ? (total + TILE - 1) / TILE : 0, warp_sums, ntile);
-  const int small0 = block_scan(tid < count ? (total + SMALL - 1) / SMALL : 0, warp_sums, nsmall);
   const int my_chunks = tid < count ? max(1, (total + CHUNK - 1) / CHUNK) : 0;
-  const int chunk0 = block_scan(my_chunks, warp_sums, nchunk);
   const int my_slots = my_chunks > 1 ? my_chunks : 0;
-  const int slot0 = block_scan(my_slots, warp_sums, nslot);
+  int v[SCANS] = {total, (total + TILE - 1) / TILE, (total + SMALL - 1) / SMALL, my_chunks, my_slots, (total + SUB - 1) / SUB};
+  int all[SCANS];
+  block_scan(v, all, warp_sums);
+  const int with = all[FIRST], ntile = all[TILES], nsmall = all[SMALLS], nchunk = all[CHUNKS];
   if (tid < count) {
-    pv.start[tid] = first;
-    pv.parts[tid] = make_int2(slot0, my_slots);
-    for (int w = 0; w < PLAN_WARPS; ++w) counters[w * nb + tid] += first;
+    pv.start[tid] = v[FIRST];
+    pv.parts[tid] = make_int2(v[SLOTS], my_slots);
+    int at = v[FIRST];
+#pragma unroll
+    for (int w = 0; w < PLAN_WARPS; ++w) {
+      counters[w * nb + tid] = at;
+      at += counts[w];
+    }
   }
   if (tid == 0) {
     int at = with;                             // the tokens without an adapter come last
@@ -173,21 +184,20 @@ __global__ void __launch_bounds__(PLAN_WARPS * 32)
   // the tables, a warp per adapter: thread l's numbers go through shared memory
   __syncthreads();
   if (tid < count) {
-    counters[tid * 6] = first, counters[tid * 6 + 1] = total, counters[tid * 6 + 2] = tile0;
-    counters[tid * 6 + 3] = small0, counters[tid * 6 + 4] = chunk0, counters[tid * 6 + 5] = my_slots ? slot0 : -1;
+    int* c = counters + tid * 7;
+    c[0] = v[FIRST], c[1] = total, c[2] = v[TILES], c[3] = v[SMALLS], c[4] = v[CHUNKS];
+    c[5] = my_slots ? v[SLOTS] : -1, c[6] = v[SUBS];
   }
   __syncthreads();
   for (int l = warp; l <= count; l += PLAN_WARPS) {
     const bool none = l == count;
-    const int f = none ? with : counters[l * 6], c = none ? T - with : counters[l * 6 + 1];
-    const int t = none ? ntile : counters[l * 6 + 2], s = none ? nsmall : counters[l * 6 + 3];
+    const int* n = counters + l * 7;
+    const int f = none ? with : n[0], c = none ? T - with : n[1], t = none ? ntile : n[2], s = none ? nsmall : n[3];
     for (int i = lane; i * TILE < c; i += 32) pv.tiles[t + i] = make_int2(l, f + i * TILE);
     for (int i = lane; i * SMALL < c; i += 32) pv.small[s + i] = make_int2(l, f + i * SMALL);
-    if (!none) {
-      const int k = counters[l * 6 + 4], slot = counters[l * 6 + 5];
+    if (!none)
       for (int i = lane; i == 0 || i * CHUNK < c; i += 32)
-        pv.chunks[k + i] = make_int4(l, f + i * CHUNK, slot < 0 ? -1 : slot + i, 0);
-    }
+        pv.chunks[n[4] + i] = make_int4(l, f + i * CHUNK, n[5] < 0 ? -1 : n[5] + i, n[6] + i * (CHUNK / SUB));
   }
 }
 
@@ -258,6 +268,7 @@ struct ApplyArgs {
   int T, n, m, r, count;
   bool h_scaled;               // h gets s_l P_l x_t instead of P_l x_t
   bool vec_x, vec_p, vec_q, vec_y;   // rows that allow the kernel's vector loads
+  bool fast_y;                 // 16-byte rows of base and y at equal, 32-bit offsets (in units of 16 bytes)
 };
 
 // The plan of a call must be one made for its T and count.
@@ -448,12 +459,14 @@ __global__ void __launch_bounds__(VT)
 // memory (each CTA adds up a share of the tokens, in rank order), h goes to
 // memory.
 //
-// Expand: one CTA per tile and run of column blocks: D[token][column] = h Q
-// (M = 128 tokens, N = the block's columns, K = r, Q MN-major as it lies in
-// memory).  A TMEM lane is a token; each warp turns 32 tokens x 32 columns
-// through shared memory, so that neighbouring lanes read the base and write y
-// in whole 64- or 128-byte pieces of a row.  The base of the next block is on
-// its way while this one is multiplied.
+// Expand: resident CTAs, each an equal run of the (tile, column block) pairs:
+// D[token][column] = h Q (M = 128 tokens, N = the block's columns, K = r, Q MN-major as it lies in
+// memory).  Three warps fetch Q's tiles, one multiplies; the others, in up to
+// four groups of four, take a block in turn, 32 tokens (TMEM lanes) each: a warp
+// brings its rows of the base to shared memory, 256 bytes at a time by 16
+// neighbouring lanes, adds a row's products there, and sends the sums out as
+// the base came, while the other groups' rows are on their way.  The sides
+// meet at mbarriers only (tile of Q there, accumulator full, accumulator read).
 //
 // Types: a bf16 value is one operand piece, an fp32 value three (split3), and
 // the products of pieces of order 2 and below are formed: fp32 operands keep
@@ -462,10 +475,14 @@ __global__ void __launch_bounds__(VT)
 // The tensor core drops low bits of the running sum at every step, so the
 // blocks of n are dealt out over several accumulators that are added in fp32.
 //
-// Loads are gathered by token into shared memory with the 128-byte swizzle:
-// by cp.async, several blocks ahead, where bf16 rows allow 16-byte copies
-// (CP); else through registers one block ahead, which also cuts fp32 values
-// into pieces and takes any alignment.
+// Loads are gathered by token into shared memory with the 128-byte swizzle,
+// by cp.async where bf16 rows allow 16-byte copies (CP), else through
+// registers, which also cuts fp32 values into pieces and takes any alignment.
+// Each stage has a warp of its own that fills it, waits for it and hands it
+// on: the fence between a thread's writes and the tensor core's reads waits
+// for every load that the thread has in flight, so a thread with later stages
+// under way would wait for them at each step (2.9 us a block in the expand
+// step, whatever the rank).
 constexpr int TT = 256;                        // threads per CTA
 constexpr int TC_COLS = 256;                   // TMEM columns: two CTAs fit an SM (see shrink_smem)
 template <typename T> __host__ __device__ constexpr int pieces() { return sizeof(T) == 2 ? 1 : 3; }
@@ -474,10 +491,12 @@ constexpr int XT_BYTES = TILE * 128;           // one piece of 128 tokens x 64 c
 
 template <typename TX, typename TW>
 __host__ __device__ inline int shrink_stage(int r16) { return pieces<TX>() * XT_BYTES + pieces<TW>() * r16 * 128; }
-template <bool CP> __host__ __device__ inline int shrink_stages(int r16) { return !CP ? 2 : r16 <= 64 ? 4 : 3; }
-template <bool CP, typename TX, typename TW>
+constexpr int ST = 160;                        // threads: four warps with a stage each, one to multiply
+__host__ __device__ inline int shrink_stages(int stage) { return stage <= 24 * 1024 ? 4 : 3; }
+template <typename TX, typename TW>
 __host__ __device__ inline int shrink_smem(int r16) {
-  int s = shrink_stages<CP>(r16) * shrink_stage<TX, TW>(r16);
+  const int stage = shrink_stage<TX, TW>(r16);
+  int s = shrink_stages(stage) * stage;
   const int hp = TILE * (r16 + 4) * 4;         // the partial h, in the stages' place
   if (hp > s) s = hp;
   s += 1024;
@@ -485,22 +504,34 @@ __host__ __device__ inline int shrink_smem(int r16) {
   // a cluster ever waits for TMEM while its peers wait for it
   return s < 78 * 1024 ? 78 * 1024 : s;
 }
-// Columns of a block of the expand step, its buffers.
-template <typename TY> __host__ __device__ constexpr int expand_cols() { return sizeof(TY) == 2 ? 128 : 64; }
-constexpr int RING = 2, TURN_BYTES = 32 * 128;  // of each warp
+// A block of the expand step is 256 bytes of y's rows; Q's tiles in flight and
+// groups with a block's rows, as many as fit.
+template <typename TY> __host__ __device__ constexpr int expand_cols() { return 256 / (int)sizeof(TY); }
+constexpr int EW = 16, QW = 3, ET = 32 * (EW + QW + 1);    // warps: rows of y, tiles of Q, multiply
+constexpr int ROW_BYTES = TILE * 256, EXPAND_MAX = 226 * 1024;
+constexpr int ACCS = 4;                        // blocks' accumulators in TMEM
+struct ExpandRings {
+  int q, rows, smem;
+};
 template <typename TW, typename TY>
-__host__ __device__ inline int expand_tile(int r16) { return pieces<TW>() * r16 * 2 * expand_cols<TY>(); }
+__host__ __device__ inline int expand_tile(int r16) { return pieces<TW>() * r16 * 2 * (expand_cols<TY>() > 64 ? expand_cols<TY>() : 64); }
 template <typename TW, typename TY>
-__host__ __device__ inline int expand_smem(int r16) {
-  return h_pieces<TY>() * ((r16 + 63) / 64) * XT_BYTES + RING * expand_tile<TW, TY>(r16) + TT / 32 * TURN_BYTES + 1024;
+inline ExpandRings expand_rings(int r16) {
+  const int h = h_pieces<TY>() * ((r16 + 63) / 64) * XT_BYTES + 1024, tile = expand_tile<TW, TY>(r16);
+  ExpandRings e{QW, 4, 0};
+  while (e.q > 3 && h + e.q * tile + e.rows * ROW_BYTES > EXPAND_MAX) --e.q;
+  while (e.rows > 3 && h + e.q * tile + e.rows * ROW_BYTES > EXPAND_MAX) --e.rows;
+  while (e.q > 2 && h + e.q * tile + e.rows * ROW_BYTES > EXPAND_MAX) --e.q;
+  while (e.rows > 1 && h + e.q * tile + e.rows * ROW_BYTES > EXPAND_MAX) --e.rows;
+  e.smem = h + e.q * tile + e.rows * ROW_BYTES;
+  return e;
 }
 
 __device__ __forceinline__ void cp16(uint8_t* dst, const void* src, bool there) {   // 16 bytes, or zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Eight consecutive values in registers.
 template <typename T> struct Eight;
@@ -556,14 +587,14 @@ template <> struct Eight<float> {
 // that takes the small terms of operands in pieces.
 __host__ __device__ constexpr int tc_accs(int r16) { return r16 <= 64 ? 4 : 2; }
 
-template <typename TX, typename TW, int RB, bool CP>
-__global__ void __launch_bounds__(TT, 2)
+template <typename TX, typename TW, bool CP>
+__global__ void __launch_bounds__(ST, 2)
     k_adapter_shrink(const __grid_constant__ ApplyArgs<TX, TW, float> a, void* plan) {
-  constexpr int PX = pieces<TX>(), PW = pieces<TW>(), XR = TILE * 8 / TT, PR = RB * 8 / TT;
+  constexpr int PX = pieces<TX>(), PW = pieces<TW>();
   constexpr bool SPLIT = PX > 1 || PW > 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int tok[TILE];
-  __shared__ uint64_t bars[4];
+  __shared__ uint64_t full[4], empty[4], all_done;
   __shared__ uint32_t tmem_base;
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -577,13 +608,14 @@ __global__ void __launch_bounds__(TT, 2)
   if (tid < TILE) tok[tid] = tid < cnt ? pv.order[tile.y + tid] : -1;
   if (l == a.count) {                          // no adapter: h = 0
     __syncthreads();
-    for (int i = rank * TT + tid; i < cnt * r; i += nc * TT) a.h[(int64_t)tok[i / r] * r + i % r] = 0.f;
+    for (int i = rank * ST + tid; i < cnt * r; i += nc * ST) a.h[(int64_t)tok[i / r] * r + i % r] = 0.f;
     return;
   }
-  const int r16 = (r + 15) / 16 * 16, stages = shrink_stages<CP>(r16), stage = shrink_stage<TX, TW>(r16);
+  const int r16 = (r + 15) / 16 * 16, stage = shrink_stage<TX, TW>(r16), stages = shrink_stages(stage);
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    mbar_init(&all_done, 1);
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&tmem_base, TC_COLS);
@@ -593,106 +625,79 @@ __global__ void __launch_bounds__(TT, 2)
   const uint32_t tmem = tmem_base;
   bool ok = true;                  // a wait that ran out is the last: what follows it is not stored
   const TW* P = a.P + (int64_t)l * r * a.n;
-
-  // this CTA's 64-column blocks [k0, k1)
+  // this CTA's 64-column blocks [k0, k0 + steps)
   const int blocks = (a.n + 63) / 64, per = (blocks + nc - 1) / nc;
   const int k0 = min(blocks, rank * per), steps = min(blocks, k0 + per) - k0;
   const int accs = tc_accs(r16), mains = SPLIT ? accs - 1 : accs;
-  const int ch = tid % 8, row0 = tid / 8;      // this thread's 16-byte column and first row of a block
-  auto spot = [&](int row) { return row * 128 + ((ch ^ (row & 7)) << 4); };
-  const uint32_t idesc = make_idesc_bf16(TILE, r16, 0, 0);
-  auto multiply = [&](int i, int s) {          // one thread
-    const uint32_t xa = smem_u32(sm + s * stage), pa = xa + PX * XT_BYTES;
-    bool small = i > 0;                        // the small terms' accumulator holds something
-#pragma unroll
-    for (int px = 0; px < PX; ++px)
-#pragma unroll
-      for (int pw = 0; pw < PW && px + pw <= 2; ++pw) {
-        const bool main = px + pw == 0;
-        const uint32_t d = tmem + (uint32_t)((main ? i % mains : accs - 1) * r16);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_f16(d, make_sw128_desc(xa + px * XT_BYTES + kk * 32, 16, 1024),
-                     make_sw128_desc(pa + pw * r16 * 128 + kk * 32, 16, 1024), idesc,
-                     (main ? i >= mains : small) || kk > 0);
-        if (!main) small = true;
-      }
-    tc_commit(&bars[s]);
-  };
-  if constexpr (CP) {
-    auto fill = [&](int i) {
-      if (i < steps) {
-        uint8_t* xs = sm + (i % stages) * stage;
-        const int c = 64 * (k0 + i) + 8 * ch;
-#pragma unroll
-        for (int j = 0; j < XR; ++j) {
-          const int row = row0 + j * (TT / 8), t = tok[row];
-          // a row past the tile's tokens only feeds its own sums: nothing is loaded
-          if (t >= 0) cp16(xs + spot(row), a.x + (int64_t)t * a.ldx + (c < a.n ? c : 0), c < a.n);
+  if (warp < 4) {
+    if (warp < stages) {
+      const int ch = lane % 8, row0 = lane / 8;    // the lane's 16-byte column and first row
+      uint8_t* xs = sm + warp * stage;
+      uint8_t* ps = xs + PX * XT_BYTES;
+      auto spot = [&](int row) { return row * 128 + ((ch ^ (row & 7)) << 4); };
+      for (int i = warp; i < steps; i += stages) {
+        if (i >= stages) ok = ok && mbar_wait(&empty[warp], (uint32_t)((i / stages - 1) & 1));
+        const int c = 64 * (k0 + i) + 8 * ch, left = a.n - c;
+        if constexpr (CP) {
+          const __nv_bfloat16* x = a.x + (c < a.n ? c : 0);
+#pragma unroll 8
+          for (int row = row0; row < cnt; row += 4)    // rows past the tile's tokens only feed their own sums
+            cp16(xs + spot(row), x + (int64_t)tok[row] * a.ldx, c < a.n);
+#pragma unroll 4
+          for (int row = row0; row < r16; row += 4) {
+            const bool there = row < r && c < a.n;
+            cp16(ps + spot(row), P + (there ? (int64_t)row * a.n + c : 0), there);
+          }
+          cp_wait_all();
+        } else {
+#pragma unroll 4
+          for (int row = row0; row < TILE; row += 4) {
+            Eight<TX> v;
+            v.zero();
+            if (row < cnt && left > 0) v.load(a.x + (int64_t)tok[row] * a.ldx + c, a.vec_x, left);
+            v.store(xs + spot(row), XT_BYTES);
+          }
+#pragma unroll 4
+          for (int row = row0; row < r16; row += 4) {
+            Eight<TW> v;
+            v.zero();
+            if (row < r && left > 0) v.load(P + (int64_t)row * a.n + c, a.vec_p, left);
+            v.store(ps + spot(row), r16 * 128);
+          }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[warp]);
+      }
+    }
+  } else if (lane == 0) {
+    const uint32_t idesc = make_idesc_bf16(TILE, r16, 0, 0);
+    for (int i = 0; i < steps && ok; ++i) {
+      const int s = i % stages;
+      ok = mbar_wait(&full[s], (uint32_t)((i / stages) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t xa = smem_u32(sm + s * stage), pa = xa + PX * XT_BYTES;
+      bool small = i > 0;                      // the small terms' accumulator holds something
 #pragma unroll
-        for (int j = 0; j < PR; ++j) {
-          const int row = row0 + j * (TT / 8);
-          const bool there = row < r && c < a.n;
-          if (row < r16) cp16(xs + XT_BYTES + spot(row), P + (there ? (int64_t)row * a.n + c : 0), there);
+      for (int px = 0; px < PX; ++px)
+#pragma unroll
+        for (int pw = 0; pw < PW && px + pw <= 2; ++pw) {
+          const bool main = px + pw == 0;
+          const uint32_t d = tmem + (uint32_t)((main ? i % mains : accs - 1) * r16);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16(d, make_sw128_desc(xa + px * XT_BYTES + kk * 32, 16, 1024),
+                       make_sw128_desc(pa + pw * r16 * 128 + kk * 32, 16, 1024), idesc,
+                       (main ? i >= mains : small) || kk > 0);
+          if (!main) small = true;
         }
-      }
-      cp_commit();
-    };
-    for (int i = 0; i < stages - 1; ++i) fill(i);
-    for (int i = 0; i < steps; ++i) {
-      if (stages == 4) cp_wait<2>();
-      else cp_wait<1>();
-      fence_proxy_async_smem();
-      __syncthreads();
-      if (tid == 0 && ok) multiply(i, i % stages);
-      // the stage of the step before is the next to be filled
-      if (i > 0) ok = ok && mbar_wait(&bars[(i - 1) % stages], (uint32_t)(((i - 1) / stages) & 1));
-      fill(i + stages - 1);
+      tc_commit(&empty[s]);
     }
-    cp_wait<0>();
-    if (steps > 0) ok = ok && mbar_wait(&bars[(steps - 1) % stages], (uint32_t)(((steps - 1) / stages) & 1));
-  } else {
-    Eight<TX> xr[XR];
-    Eight<TW> pr[PR];
-    auto load = [&](int i) {
-      const int c = 64 * (k0 + i) + 8 * ch, left = a.n - c;
-#pragma unroll
-      for (int j = 0; j < XR; ++j) {
-        const int t = tok[row0 + j * (TT / 8)];
-        xr[j].zero();
-        if (t >= 0 && left > 0) xr[j].load(a.x + (int64_t)t * a.ldx + c, a.vec_x, left);
-      }
-#pragma unroll
-      for (int j = 0; j < PR; ++j) {
-        const int row = row0 + j * (TT / 8);
-        pr[j].zero();
-        if (row < r && left > 0) pr[j].load(P + (int64_t)row * a.n + c, a.vec_p, left);
-      }
-    };
-    if (steps > 0) load(0);
-    for (int i = 0; i < steps; ++i) {
-      const int s = i & 1;
-      if (i >= 2) ok = ok && mbar_wait(&bars[s], (uint32_t)(((i >> 1) - 1) & 1));
-      uint8_t* xs = sm + s * stage;
-#pragma unroll
-      for (int j = 0; j < XR; ++j) xr[j].store(xs + spot(row0 + j * (TT / 8)), XT_BYTES);
-#pragma unroll
-      for (int j = 0; j < PR; ++j) {
-        const int row = row0 + j * (TT / 8);
-        if (row < r16) pr[j].store(xs + PX * XT_BYTES + spot(row), r16 * 128);
-      }
-      if (i + 1 < steps) load(i + 1);
-      fence_proxy_async_smem();
-      __syncthreads();
-      if (tid == 0 && ok) multiply(i, s);
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int used = (steps + 1 - s) / 2;
-      if (used > 0) ok = ok && mbar_wait(&bars[s], (uint32_t)((used - 1) & 1));
-    }
+    if (steps > 0 && ok) tc_commit(&all_done);
   }
+  __syncwarp();
+  if (steps > 0) ok = ok && mbar_wait(&all_done, 0u);
   __syncthreads();
   tc_fence_after();
   // ---- the partial sums of the cluster's CTAs
@@ -724,7 +729,7 @@ __global__ void __launch_bounds__(TT, 2)
   {
     const int share = (cnt + nc - 1) / nc, t0 = min(cnt, rank * share), t1 = min(cnt, t0 + share), quads = r16 / 4;
     const float scale = a.h_scaled && a.scale ? a.scale[l] : 1.f;
-    for (int i = tid; i < (t1 - t0) * quads; i += TT) {
+    for (int i = tid; i < (t1 - t0) * quads; i += ST) {
       const int t = t0 + i / quads, j = 4 * (i % quads);
       float4 w[8];
 #pragma unroll
@@ -788,202 +793,257 @@ __device__ __forceinline__ uint4 add_vec(const uint4& b, const float* v, __nv_bf
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// `per`: column blocks of a CTA.  a.h as the shrink step left it, times the
-// scale already where a.h_scaled.
-template <typename TW, typename TY, int RB, bool CP>
-__global__ void __launch_bounds__(TT, 2)
-    k_adapter_expand(const __grid_constant__ ApplyArgs<float, TW, TY> a, int per, void* plan) {
-  constexpr int PW = pieces<TW>(), NP = h_pieces<TY>(), CB = expand_cols<TY>();
-  constexpr int CH = CB / 8, QROWS = TT / CH, QR = RB / QROWS, EV = 16 / (int)sizeof(TY);
-  constexpr int LANES = 32 / EV, ROWS = 32 / LANES;       // lanes on 32 columns of a row; rows at once
+// a.h as the shrink step left it, times the scale already where a.h_scaled.
+template <typename TW, typename TY, bool CP>
+__global__ void __launch_bounds__(ET, 1)
+    k_adapter_expand(const __grid_constant__ ApplyArgs<float, TW, TY> a, ExpandRings rings, void* plan) {
+  constexpr int PW = pieces<TW>(), NP = h_pieces<TY>(), CB = expand_cols<TY>(), EV = 16 / (int)sizeof(TY);
+  constexpr int CH = CB / 8, TCOLS = ACCS * CB;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int tok[TILE];
-  __shared__ uint64_t bars[2];
+  __shared__ uint64_t full[ACCS], read[ACCS], there[QW];
   __shared__ uint32_t tmem_base;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = a.r;
   // The launch before released this one after its own wait: all but h is there.
   const PlanView pv = plan_view(plan, a.T, a.count);
-  const bool mine = plan_ok(pv, a.T, a.count) && (int)blockIdx.y < pv.head[H_TILES];
-  const int2 tile = mine ? pv.tiles[blockIdx.y] : make_int2(0, 0);
-  const int l = tile.x, cnt = mine ? min(TILE, pv.start[l + 1] - tile.y) : 0;
-  const int blocks = (a.m + CB - 1) / CB, b0 = blockIdx.x * per, steps = min(blocks, b0 + per) - b0;
-  // this warp's 32 tokens of a tile and CB / 2 columns of a block; of these
-  // vector v of the lane is 16 bytes of 32 columns (v / LANES) of row
-  // (v % LANES) ROWS + lane / LANES
-  const int token0 = 32 * (warp % 4), col = (warp / 4) * (CB / 2);
-  auto vrow = [&](int v) { return token0 + (v % LANES) * ROWS + lane / LANES; };
-  auto vcol = [&](int v) { return col + v / LANES * 32 + lane % LANES * EV; };
-  if (tid < TILE) tok[tid] = tid < cnt ? pv.order[tile.y + tid] : -1;
-  __syncthreads();
-  uint4 base[8];
-  auto load_base = [&](int i) {
-#pragma unroll
-    for (int v = 0; v < 8; ++v) {
-      const int t = vrow(v), c = (b0 + i) * CB + vcol(v);
-      base[v] = make_uint4(0u, 0u, 0u, 0u);
-      if (t < cnt && a.base) base[v] = load_vec(a.base + (int64_t)tok[t] * a.ldb + c, a.vec_y, a.m - c);
-    }
-  };
-  if (!mine || l == a.count) {
-    pdl_wait_then_release();
-    if (mine && a.y != a.base)                 // no adapter: y = base
-      for (int i = 0; i < steps; ++i) {
-        load_base(i);
-#pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          const int t = vrow(v), c = (b0 + i) * CB + vcol(v);
-          if (t < cnt) store_vec(a.y + (int64_t)tok[t] * a.ldy + c, base[v], a.vec_y, a.m - c);
-        }
-      }
-    return;
-  }
+  const bool mine = plan_ok(pv, a.T, a.count);
+  const int blocks = (a.m + CB - 1) / CB;
+  const int64_t work = mine ? (int64_t)pv.head[H_TILES] * blocks : 0;
+  const int64_t w0 = work * blockIdx.x / gridDim.x, w1 = work * (blockIdx.x + 1) / gridDim.x;
   const int r16 = (r + 15) / 16 * 16, kb = (r16 + 63) / 64, qtile = expand_tile<TW, TY>(r16);
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qs = sm + NP * kb * XT_BYTES;
-  float4* turn = reinterpret_cast<float4*>(qs + RING * qtile + warp * TURN_BYTES);
-  const TW* Q = a.Q + (int64_t)l * r * a.m;
-  const int ch = tid % CH, j0 = tid / CH;      // this thread's 16-byte column and first row of a tile of Q
-  // MN-major: 64-column boxes of r16 rows x 128 bytes
-  auto spot = [&](int j) { return (ch / 8) * (r16 * 128) + j * 128 + (((ch % 8) ^ (j & 7)) << 4); };
-  auto fill = [&](int i) {
-    if (i < steps) {
-      const int c = (b0 + i) * CB + 8 * ch;
-#pragma unroll
-      for (int q = 0; q < QR; ++q) {
-        const int j = j0 + q * QROWS;
-        const bool there = j < r && c < a.m;
-        if (j < r16) cp16(qs + (i % RING) * qtile + spot(j), Q + (there ? (int64_t)j * a.m + c : 0), there);
-      }
-    }
-    cp_commit();
-  };
-  Eight<TW> qr[CP ? 1 : QR];
-  auto load_q = [&](int i) {
-    const int c = (b0 + i) * CB + 8 * ch, left = a.m - c;
-#pragma unroll
-    for (int q = 0; q < (CP ? 0 : QR); ++q) {
-      const int j = j0 + q * QROWS;
-      qr[q].zero();
-      if (j < r && left > 0) qr[q].load(Q + (int64_t)j * a.m + c, a.vec_q, left);
-    }
-  };
-  if constexpr (CP) {
-    fill(0);
-  } else {
-    load_q(0);
-  }
-  load_base(0);
   if (tid == 0) {
-    mbar_init(&bars[0], 1);
-    mbar_init(&bars[1], 1);
+    for (int i = 0; i < ACCS; ++i) mbar_init(&full[i], 1), mbar_init(&read[i], 4);
+    for (int i = 0; i < QW; ++i) mbar_init(&there[i], 1);
     fence_mbar_init();
   }
-  if (warp == 0) tmem_alloc(&tmem_base, 2 * CB);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_base;
-  bool ok = true;
-  pdl_wait_then_release();
-  // ---- the pieces of scale h, K-major, 64 ranks to a block
-  {
-    const float scale = a.scale && !a.h_scaled ? a.scale[l] : 1.f;
-    const int eights = r16 / 8;
-    for (int i = tid; i < cnt * eights; i += TT) {
-      const int t = i / eights, c = i % eights;
-      const float* h = a.h + (int64_t)tok[t] * r + 8 * c;
-      float f[8];
-      if (r % 4 == 0 && (reinterpret_cast<uintptr_t>(a.h) & 15) == 0) {
-        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 u = 8 * c < r ? *reinterpret_cast<const float4*>(h) : z;
-        const float4 w = 8 * c + 4 < r ? *reinterpret_cast<const float4*>(h + 4) : z;
-        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = w.x, f[5] = w.y, f[6] = w.z, f[7] = w.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = 8 * c + e < r ? h[e] : 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] *= scale;
-      store_pieces<NP>(sm + (c / 8) * XT_BYTES + t * 128 + (((c % 8) ^ (t & 7)) << 4), kb * XT_BYTES, f);
-    }
-  }
+  uint32_t tmem = 0;
+  bool ok = true, started = false;             // the wait for h, and TMEM
+  int done = 0;                                // blocks multiplied so far: accumulator, phase and tile of the next
   const uint32_t idesc = make_idesc_bf16(TILE, CB, 0, 1);
-  for (int i = 0; i <= steps; ++i) {
-    if (i < steps) {
-      uint8_t* q = qs + (i % RING) * qtile;
-      if constexpr (CP) {
-        cp_wait<0>();
-      } else {
+  for (int64_t w = w0; w < w1;) {
+    const int2 tile = pv.tiles[w / blocks];
+    const int l = tile.x, cnt = min(TILE, pv.start[l + 1] - tile.y);
+    const int b0 = (int)(w % blocks), steps = (int)min((int64_t)(blocks - b0), w1 - w);
+    w += steps;
+    __syncthreads();                           // the tile before is done with tok and h's pieces
+    if (tid < TILE) tok[tid] = tid < cnt ? pv.order[tile.y + tid] : -1;
+    __syncthreads();
+    // Group warp / 4, 32 tokens.  To and from memory a lane moves 16 bytes, 16
+    // lanes to a row, of rows 2 v + lane / 16.
+    const int token0 = 32 * (warp % 4), group = warp / 4, col = lane % 16 * EV;
+    const bool busy = group < rings.rows && token0 < cnt;
+    uint8_t* rows = qs + rings.q * qtile + warp * 8192;    // 32 rows of 256 bytes
+    auto piece = [&](int tr, int p) { return tr * 256 + ((p ^ (tr & 7)) << 4); };
+    // Whole blocks of 32 tokens that are all there go by offsets kept in
+    // registers (9 instructions in 16 bytes would be spent on them otherwise).
+    const bool fast = a.fast_y && busy && token0 + 32 <= cnt && l != a.count;
+    uint32_t offset[16];
 #pragma unroll
-        for (int k = 0; k < QR; ++k) {
-          const int j = j0 + k * QROWS;
-          if (j < r16) qr[k].store(q + spot(j), r16 * 2 * CB);
+    for (int v = 0; v < 16; ++v)
+      offset[v] = fast ? (uint32_t)(tok[token0 + 2 * v + lane / 16] * (a.ldy / EV)) + lane % 16 : 0u;
+    auto fill_rows = [&](int i) {
+      if (fast && i < steps && (b0 + i + 1) * CB <= a.m) {
+        const uint4* from = reinterpret_cast<const uint4*>(a.base) + (b0 + i) * (CB / EV);
+        const uint32_t to = smem_u32(rows) + lane / 16 * 256;
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           to + v * 512 + (((lane % 16) ^ ((2 * v + lane / 16) & 7)) << 4)),
+                       "l"(from + offset[v])
+                       : "memory");
+      } else if (i < steps && a.base && busy) {
+        const int c = (b0 + i) * CB + col, left = a.m - c;
+#pragma unroll 2
+        for (int v = 0; v < 16; ++v) {
+          const int tr = 2 * v + lane / 16, t = tok[token0 + tr];
+          if (t < 0) continue;
+          const TY* from = a.base + (int64_t)t * a.ldb + c;
+          if (a.vec_y && left >= EV) cp16(rows + piece(tr, lane % 16), from, true);
+          else *reinterpret_cast<uint4*>(rows + piece(tr, lane % 16)) = load_vec(from, false, left);
         }
-        if (i + 1 < steps) load_q(i + 1);
+      }
+    };
+    const TW* Q = a.Q + (int64_t)l * r * a.m;
+    // warp EW + q fills the q-th tile of the ring, for blocks n = q modulo the ring
+    auto fill_q = [&](int i) {
+      const int ch = lane % CH, c = (b0 + i) * CB + 8 * ch;
+      uint8_t* to = qs + (warp - EW) * qtile;
+      // MN-major boxes of 64 columns, 128 bytes to a row
+      auto spot = [&](int j) { return (ch / 8) * (r16 * 128) + j * 128 + (((ch % 8) ^ (j & 7)) << 4); };
+      if constexpr (CP) {
+        const TW* from = Q + (c < a.m ? c : 0);
+#pragma unroll 8
+        for (int j = lane / CH; j < r16; j += 32 / CH) {
+          const bool in = j < r && c < a.m;
+          cp16(to + spot(j), from + (in ? (int64_t)j * a.m : 0), in);
+        }
+        cp_wait_all();
+      } else {
+#pragma unroll 4
+        for (int j = lane / CH; j < r16; j += 32 / CH) {
+          Eight<TW> v;
+          v.zero();
+          if (j < r && c < a.m) v.load(Q + (int64_t)j * a.m + c, a.vec_q, a.m - c);
+          v.store(to + spot(j), r16 * 2 * (CB > 64 ? CB : 64));
+        }
       }
       fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&there[warp - EW]);
+    };
+    // the first block of this run whose tile this warp fills
+    const int q0 = warp >= EW && warp < EW + rings.q ? ((warp - EW - done) % rings.q + rings.q) % rings.q : steps;
+    if (l != a.count) {
+      if (warp < EW) fill_rows(group);
+      else if (q0 < steps) fill_q(q0);
+    }
+    if (!started) {                            // TMEM only now: the launch before may still need it
+      started = true;
+      pdl_wait_then_release();
+      if (warp == 0) tmem_alloc(&tmem_base, TCOLS);
       tc_fence_before();
       __syncthreads();
-      if (tid == 0 && ok) {
-        tc_fence_after();
-        const uint32_t qa = smem_u32(q), ha = smem_u32(sm), d = tmem + (uint32_t)((i & 1) * CB);
-        bool first = true;
-#pragma unroll
-        for (int ph = NP - 1; ph >= 0; --ph)   // the small terms first
-#pragma unroll
-          for (int pw = PW - 1; pw >= 0; --pw) {
-            if (ph + pw > 2) continue;
-            for (int k = 0; k < r16 / 16; ++k) {
-              tc_mma_f16(d, make_sw128_desc(ha + (ph * kb + k / 4) * XT_BYTES + (k % 4) * 32, 16, 1024),
-                         make_sw128_desc(qa + pw * r16 * 2 * CB + k * 2048, r16 * 128, 1024), idesc, !first);
-              first = false;
-            }
-          }
-        tc_commit(&bars[i & 1]);
-      }
-    }
-    if (i > 0) ok = ok && mbar_wait(&bars[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1));
-    if constexpr (CP) fill(i + 1);             // into the tile that step i - 1 has read
-    if (i > 0) {                               // y of the block before, while the tensor core goes on
       tc_fence_after();
-      const uint32_t at = tmem + ((uint32_t)token0 << 16) + (uint32_t)(((i - 1) & 1) * CB + col);
-      if (token0 < cnt) {
+      tmem = tmem_base;
+    }
+    if (l == a.count) {                        // no adapter: y = base
+      if (a.y != a.base && group < EW / 4 && token0 < cnt)
+        for (int i = group; i < steps; i += EW / 4) {
+          const int c = (b0 + i) * CB + col, left = a.m - c;
 #pragma unroll
-        for (int g = 0; g < CB / 64; ++g) {
-          float v[32];
-          tmem_ld32(at + 32 * g, v);
-          // row `lane`, 16-byte pieces swizzled by the row
+          for (int h = 0; h < 2; ++h) {        // eight loads in flight
+            uint4 u[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            turn[lane * 8 + (k ^ (lane & 7))] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < LANES; ++k) {
-            const int e = g * LANES + k, t = vrow(e), c = (b0 + i - 1) * CB + vcol(e);
-            const int tr = t - token0, piece = lane % LANES * (EV / 4);
-            float d[EV];
-#pragma unroll
-            for (int p = 0; p < EV / 4; ++p) {
-              const float4 f = turn[tr * 8 + ((piece + p) ^ (tr & 7))];
-              d[4 * p] = f.x, d[4 * p + 1] = f.y, d[4 * p + 2] = f.z, d[4 * p + 3] = f.w;
+            for (int v = 0; v < 8; ++v) {
+              const int64_t t = tok[token0 + 16 * h + 2 * v + lane / 16];
+              u[v] = t >= 0 && a.base ? load_vec(a.base + t * a.ldb + c, a.vec_y, left) : make_uint4(0u, 0u, 0u, 0u);
             }
-            if (t < cnt && ok)
-              store_vec(a.y + (int64_t)tok[t] * a.ldy + c, add_vec(base[e], d, TY()), a.vec_y, a.m - c);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              const int64_t t = tok[token0 + 16 * h + 2 * v + lane / 16];
+              if (t >= 0) store_vec(a.y + t * a.ldy + c, u[v], a.vec_y, left);
+            }
           }
-          __syncwarp();
+        }
+      continue;
+    }
+    // ---- the pieces of scale h, K-major, 64 ranks to a block
+    if (warp < EW) {
+      const float scale = a.scale && !a.h_scaled ? a.scale[l] : 1.f;
+      const int eights = r16 / 8;
+      const bool vec_h = r % 4 == 0 && (reinterpret_cast<uintptr_t>(a.h) & 15) == 0;
+      for (int i = tid; i < cnt * eights; i += 32 * EW) {
+        const int t = i / eights, c = i % eights;
+        const float* h = a.h + (int64_t)tok[t] * r + 8 * c;
+        float f[8];
+        if (vec_h) {
+          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 u = 8 * c < r ? *reinterpret_cast<const float4*>(h) : z;
+          const float4 v = 8 * c + 4 < r ? *reinterpret_cast<const float4*>(h + 4) : z;
+          f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = 8 * c + e < r ? h[e] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= scale;
+        store_pieces<NP>(sm + (c / 8) * XT_BYTES + t * 128 + (((c % 8) ^ (t & 7)) << 4), kb * XT_BYTES, f);
+      }
+      fence_proxy_async_smem();
+    }
+    __syncthreads();
+    if (warp == EW + QW) {
+      if (lane == 0) {
+        const uint64_t ha = make_sw128_desc(smem_u32(sm), 16, 1024);
+        for (int i = 0; i < steps && ok; ++i) {
+          const int n = done + i, b = n % ACCS, s = n % rings.q;
+          ok = mbar_wait(&there[s], (uint32_t)((n / rings.q) & 1));
+          if (n >= ACCS) ok = ok && mbar_wait(&read[b], (uint32_t)((n / ACCS - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t qa = make_sw128_desc(smem_u32(qs + s * qtile), r16 * 128, 1024);
+          const uint32_t d = tmem + (uint32_t)(b * CB);
+          bool first = true;
+#pragma unroll
+          for (int ph = NP - 1; ph >= 0; --ph)           // the small terms first
+#pragma unroll
+            for (int pw = PW - 1; pw >= 0; --pw) {
+              if (ph + pw > 2) continue;
+              for (int k = 0; k < r16 / 16; ++k) {
+                // descriptors' addresses count 16 bytes
+                tc_mma_f16(d, ha + (uint64_t)(((ph * kb + k / 4) * XT_BYTES + (k % 4) * 32) >> 4),
+                           qa + (uint64_t)((pw * r16 * 2 * (CB > 64 ? CB : 64) + k * 2048) >> 4), idesc, !first);
+                first = false;
+              }
+            }
+          tc_commit(&full[b]);
         }
       }
-      tc_fence_before();
+      __syncwarp();
+    } else if (warp >= EW) {
+      for (int i = q0 + rings.q; i < steps; i += rings.q) {
+        const int back = done + i - rings.q;   // the block that read this tile
+        ok = ok && mbar_wait(&full[back % ACCS], (uint32_t)((back / ACCS) & 1));
+        fill_q(i);
+      }
+    } else {
+      for (int i = group; group < rings.rows && i < steps; i += rings.rows) {
+        const int n = done + i, b = n % ACCS;
+        cp_wait_all();
+        __syncwarp();
+        ok = ok && mbar_wait(&full[b], (uint32_t)((n / ACCS) & 1));
+        tc_fence_after();
+        if (busy) {
+          const uint32_t at = tmem + ((uint32_t)token0 << 16) + (uint32_t)(b * CB);
+#pragma unroll
+          for (int g = 0; g < CB / 32; ++g) {
+            float d[32];
+            tmem_ld32(at + 32 * g, d);
+#pragma unroll
+            for (int p = 0; p < 32 / EV; ++p) {
+              uint4* e = reinterpret_cast<uint4*>(rows + lane * 256 + (((g * (32 / EV) + p) ^ (lane & 7)) << 4));
+              *e = add_vec(a.base ? *e : make_uint4(0u, 0u, 0u, 0u), d + p * EV, TY());
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&read[b]);
+        if (fast && ok && (b0 + i + 1) * CB <= a.m) {
+          uint4* to = reinterpret_cast<uint4*>(a.y) + (b0 + i) * (CB / EV);
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            to[offset[v]] = *reinterpret_cast<const uint4*>(rows + piece(2 * v + lane / 16, lane % 16));
+        } else if (busy && ok) {
+          const int c = (b0 + i) * CB + col, left = a.m - c;
+#pragma unroll 2
+          for (int v = 0; v < 16; ++v) {
+            const int tr = 2 * v + lane / 16, t = tok[token0 + tr];
+            if (t >= 0)
+              store_vec(a.y + (int64_t)t * a.ldy + c,
+                        *reinterpret_cast<const uint4*>(rows + piece(tr, lane % 16)), a.vec_y, left);
+          }
+        }
+        __syncwarp();                          // the group's next rows go there
+        fill_rows(i + rings.rows);
+      }
     }
-    if (i > 0 && i < steps) load_base(i);
+    cp_wait_all();
+    done += steps;
   }
-  if constexpr (CP) cp_wait<0>();
+  if (!started) {
+    pdl_wait_then_release();
+    return;
+  }
+  // every multiplication is over: its accumulator was waited for
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * CB);
+    tmem_dealloc(tmem, TCOLS);
   }
 }
 

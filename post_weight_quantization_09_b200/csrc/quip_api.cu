@@ -1943,53 +1943,55 @@ bool rows_of_eight(const void* p, int64_t ld, size_t size) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
 }
 
-template <int RB, bool CP, typename TX, typename TW>
+template <bool CP, typename TX, typename TW>
 cudaError_t adapter_shrink(const ad::ApplyArgs<TX, TW, float>& a, void* plan, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  auto* kernel = ad::k_adapter_shrink<TX, TW, RB, CP>;
-  cudaError_t e = allow_smem(kernel, std::max(ad::shrink_smem<CP, TX, TW>(RB), ad::shrink_smem<CP, TX, TW>(64)), done);
+  auto* kernel = ad::k_adapter_shrink<TX, TW, CP>;
+  cudaError_t e = allow_smem(kernel, 226 * 1024, done);
   if (e != cudaSuccess) return e;
   // CTAs per cluster: as many as fill two per SM, each with a few blocks
   const int64_t likely = (a.T + ad::TILE - 1) / ad::TILE, blocks = (a.n + 63) / 64;
   unsigned nc = 1;
   while (nc < 8 && likely * nc < 2 * (int64_t)num_sms() && nc * 2 <= blocks) nc *= 2;
   LaunchScope ls("k_adapter_shrink", st);
-  return launch_cluster(kernel, (unsigned)(ad::max_tiles(a.T, a.count, ad::TILE) * nc), ad::TT,
-                        ad::shrink_smem<CP, TX, TW>((a.r + 15) / 16 * 16), nc, true, st, a, plan);
+  return launch_cluster(kernel, (unsigned)(ad::max_tiles(a.T, a.count, ad::TILE) * nc), ad::ST,
+                        ad::shrink_smem<TX, TW>((a.r + 15) / 16 * 16), nc, true, st, a, plan);
 }
 
-template <int RB, bool CP, typename TW, typename TY>
+template <bool CP, typename TW, typename TY>
 cudaError_t adapter_expand(const ad::ApplyArgs<float, TW, TY>& a, void* plan, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  auto* kernel = ad::k_adapter_expand<TW, TY, RB, CP>;
-  cudaError_t e = allow_smem(kernel, ad::expand_smem<TW, TY>(RB), done);
+  auto* kernel = ad::k_adapter_expand<TW, TY, CP>;
+  cudaError_t e = allow_smem(kernel, ad::EXPAND_MAX, done);
   if (e != cudaSuccess) return e;
-  // column blocks per CTA: about six CTAs per SM in all, so that the last
-  // ones to run are short, and at most 16 blocks to a CTA's start
-  const int64_t tiles = (a.T + ad::TILE - 1) / ad::TILE, blocks = (a.m + ad::expand_cols<TY>() - 1) / ad::expand_cols<TY>();
-  const int per = (int)std::min<int64_t>(16, std::max<int64_t>(1, tiles * blocks / (6 * num_sms())));
-  const dim3 grid((unsigned)((blocks + per - 1) / per), (unsigned)ad::max_tiles(a.T, a.count, ad::TILE));
+  const ad::ExpandRings rings = ad::expand_rings<TW, TY>((a.r + 15) / 16 * 16);
+  // one CTA per SM; no more than there are blocks in tiles that may exist
+  const int64_t tiles = std::min<int64_t>(a.T, ad::max_tiles(a.T, a.count, ad::TILE));
+  const int64_t blocks = (a.m + ad::expand_cols<TY>() - 1) / ad::expand_cols<TY>();
+  const unsigned grid = (unsigned)std::min<int64_t>(num_sms(), tiles * blocks);
   LaunchScope ls("k_adapter_expand", st);
-  return launch_pdl(kernel, grid, dim3(ad::TT), ad::expand_smem<TW, TY>((a.r + 15) / 16 * 16), st, a, per, plan);
+  return launch_pdl(kernel, dim3(grid), dim3(ad::ET), rings.smem, st, a, rings, plan);
 }
 
-template <int RB, typename TX, typename TW, typename TY>
+template <typename TX, typename TW, typename TY>
 cudaError_t adapter_tc(const ad::ApplyArgs<TX, TW, TY>& a, void* plan, cudaStream_t st) {
   const bool vec_y = rows_of_eight(a.y, a.T > 1 ? a.ldy : 8, sizeof(TY)) &&
                      (!a.base || rows_of_eight(a.base, a.T > 1 ? a.ldb : 8, sizeof(TY)));
+  const bool fast_y = vec_y && a.base && (a.T == 1 || a.ldb == a.ldy) &&
+                      a.T * a.ldy * (int64_t)sizeof(TY) / 16 < (int64_t(1) << 31);
   const ad::ApplyArgs<TX, TW, float> s{a.x, a.ldx, a.P, nullptr, a.scale, nullptr, 0, nullptr, 0, a.h, a.T, a.n, a.m,
-                                       a.r, a.count, a.h_scaled, a.vec_x, a.vec_p, false, false};
+                                       a.r, a.count, a.h_scaled, a.vec_x, a.vec_p, false, false, false};
   const ad::ApplyArgs<float, TW, TY> x{nullptr, 0, nullptr, a.Q, a.scale, a.base, a.ldb, a.y, a.ldy, a.h, a.T, a.n, a.m,
-                                       a.r, a.count, a.h_scaled, false, false, a.vec_q, vec_y};
+                                       a.r, a.count, a.h_scaled, false, false, a.vec_q, vec_y, fast_y};
   constexpr bool bf = sizeof(TX) == 2 && sizeof(TW) == 2;
   cudaError_t e;
-  if constexpr (bf) e = a.vec_x && a.vec_p ? adapter_shrink<RB, true>(s, plan, st) : adapter_shrink<RB, false>(s, plan, st);
-  else e = adapter_shrink<RB, false>(s, plan, st);
+  if constexpr (bf) e = a.vec_x && a.vec_p ? adapter_shrink<true>(s, plan, st) : adapter_shrink<false>(s, plan, st);
+  else e = adapter_shrink<false>(s, plan, st);
   if (e != cudaSuccess || !a.y) return e;
   if constexpr (sizeof(TW) == 2)
-    return a.vec_q ? adapter_expand<RB, true>(x, plan, st) : adapter_expand<RB, false>(x, plan, st);
+    return a.vec_q ? adapter_expand<true>(x, plan, st) : adapter_expand<false>(x, plan, st);
   else
-    return adapter_expand<RB, false>(x, plan, st);
+    return adapter_expand<false>(x, plan, st);
 }
 
 // The tensor-core tiles serve the types that a layer's products meet (bf16
@@ -2011,9 +2013,7 @@ cudaError_t adapter_apply(ad::ApplyArgs<TX, TW, TY> a, const int32_t* ids, void*
       a.vec_x = rows_of_eight(a.x, ldx, sizeof(TX));
       a.vec_p = rows_of_eight(a.P, a.n, sizeof(TW));
       a.vec_q = rows_of_eight(a.Q, a.m, sizeof(TW));
-      if constexpr (rank > 64)
-        if (a.r > 64) return adapter_tc<128>(a, plan, st);
-      return adapter_tc<64>(a, plan, st);
+      return adapter_tc(a, plan, st);
     }
   }
   a.vec_x = rows_of_four(a.x, ldx, sizeof(TX));
@@ -2041,7 +2041,7 @@ cudaError_t adapter_typed(const AdapterCall& c, const int32_t* ids, void* plan, 
   return adapter_apply<TX, TW, TY>({static_cast<const TX*>(c.x), c.ldx, static_cast<const TW*>(c.P),
                                     static_cast<const TW*>(c.Q), c.scale, static_cast<const TY*>(c.base), c.ldb,
                                     static_cast<TY*>(c.y), c.ldy, c.h, (int)c.T, (int)c.n, (int)c.m, (int)c.r,
-                                    (int)c.count, c.h_scaled, false, false, false, false},
+                                    (int)c.count, c.h_scaled, false, false, false, false, false},
                                    ids, plan, st);
 }
 cudaError_t adapter_dispatch(int x_dtype, int w_dtype, int y_dtype, const AdapterCall& c, const int32_t* ids, void* plan,
