@@ -478,8 +478,7 @@ __global__ void __launch_bounds__(VT)
 // Loads are gathered by token into shared memory with the 128-byte swizzle,
 // by cp.async where bf16 rows allow 16-byte copies (CP), else through
 // registers, which also cuts fp32 values into pieces and takes any alignment.
-// Each stage has a warp of its own that fills it, waits for it and hands it
-// on: the fence between a thread's writes and the tensor core's reads waits
+// Each stage has warps of its own that fill it, wait for it and hand it on: the fence between a thread's writes and the tensor core's reads waits
 // for every load that the thread has in flight, so a thread with later stages
 // under way would wait for them at each step (2.9 us a block in the expand
 // step, whatever the rank).
@@ -491,7 +490,7 @@ constexpr int XT_BYTES = TILE * 128;           // one piece of 128 tokens x 64 c
 
 template <typename TX, typename TW>
 __host__ __device__ inline int shrink_stage(int r16) { return pieces<TX>() * XT_BYTES + pieces<TW>() * r16 * 128; }
-constexpr int ST = 160;                        // threads: four warps with a stage each, one to multiply
+constexpr int ST = 288;                        // threads: four pairs of warps with a stage each, a warp to multiply
 __host__ __device__ inline int shrink_stages(int stage) { return stage <= 24 * 1024 ? 4 : 3; }
 template <typename TX, typename TW>
 __host__ __device__ inline int shrink_smem(int r16) {
@@ -614,7 +613,7 @@ __global__ void __launch_bounds__(ST, 2)
   const int r16 = (r + 15) / 16 * 16, stage = shrink_stage<TX, TW>(r16), stages = shrink_stages(stage);
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&full[i], 2), mbar_init(&empty[i], 1);
     mbar_init(&all_done, 1);
     fence_mbar_init();
   }
@@ -629,36 +628,37 @@ __global__ void __launch_bounds__(ST, 2)
   const int blocks = (a.n + 63) / 64, per = (blocks + nc - 1) / nc;
   const int k0 = min(blocks, rank * per), steps = min(blocks, k0 + per) - k0;
   const int accs = tc_accs(r16), mains = SPLIT ? accs - 1 : accs;
-  if (warp < 4) {
-    if (warp < stages) {
-      const int ch = lane % 8, row0 = lane / 8;    // the lane's 16-byte column and first row
-      uint8_t* xs = sm + warp * stage;
+  if (warp < 8) {
+    const int s = warp / 2;
+    if (s < stages) {
+      const int ch = lane % 8, row0 = lane / 8 + 4 * (warp % 2);   // the lane's 16-byte column and first row
+      uint8_t* xs = sm + s * stage;
       uint8_t* ps = xs + PX * XT_BYTES;
       auto spot = [&](int row) { return row * 128 + ((ch ^ (row & 7)) << 4); };
-      for (int i = warp; i < steps; i += stages) {
-        if (i >= stages) ok = ok && mbar_wait(&empty[warp], (uint32_t)((i / stages - 1) & 1));
+      for (int i = s; i < steps; i += stages) {
+        if (i >= stages) ok = ok && mbar_wait(&empty[s], (uint32_t)((i / stages - 1) & 1));
         const int c = 64 * (k0 + i) + 8 * ch, left = a.n - c;
         if constexpr (CP) {
           const __nv_bfloat16* x = a.x + (c < a.n ? c : 0);
 #pragma unroll 8
-          for (int row = row0; row < cnt; row += 4)    // rows past the tile's tokens only feed their own sums
+          for (int row = row0; row < cnt; row += 8)    // rows past the tile's tokens only feed their own sums
             cp16(xs + spot(row), x + (int64_t)tok[row] * a.ldx, c < a.n);
 #pragma unroll 4
-          for (int row = row0; row < r16; row += 4) {
+          for (int row = row0; row < r16; row += 8) {
             const bool there = row < r && c < a.n;
             cp16(ps + spot(row), P + (there ? (int64_t)row * a.n + c : 0), there);
           }
           cp_wait_all();
         } else {
 #pragma unroll 4
-          for (int row = row0; row < TILE; row += 4) {
+          for (int row = row0; row < cnt; row += 8) {
             Eight<TX> v;
             v.zero();
-            if (row < cnt && left > 0) v.load(a.x + (int64_t)tok[row] * a.ldx + c, a.vec_x, left);
+            if (left > 0) v.load(a.x + (int64_t)tok[row] * a.ldx + c, a.vec_x, left);
             v.store(xs + spot(row), XT_BYTES);
           }
 #pragma unroll 4
-          for (int row = row0; row < r16; row += 4) {
+          for (int row = row0; row < r16; row += 8) {
             Eight<TW> v;
             v.zero();
             if (row < r && left > 0) v.load(P + (int64_t)row * a.n + c, a.vec_p, left);
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(ST, 2)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[warp]);
+        if (lane == 0) mbar_arrive(&full[s]);
       }
     }
   } else if (lane == 0) {
@@ -1117,33 +1117,80 @@ __global__ void __launch_bounds__(OT) k_adapter_outer(const __grid_constant__ Ou
 
 // The same on the tensor cores, 128 columns and all ranks (up to 128) per
 // CTA: D[column][j] = x^T u (M = 128 columns, N = r, K = tokens, x MN-major as
-// its rows lie in memory), 64 tokens at a time.  u is cut into three bf16
+// its rows lie in memory), SUB tokens at a time.  u is cut into three bf16
 // pieces; the large terms are dealt out over all accumulators but one, which
-// takes the small ones, so few steps meet in each (tc_accs).
-template <typename TX>
-__host__ __device__ inline int outer_smem(int r16) {
-  return 2 * (64 * 256 * pieces<TX>() + 3 * r16 * 128) + 1024;
+// takes the small ones, so few steps meet in each (tc_accs).  The pieces are
+// made once, K-major and swizzled as the tensor core reads them
+// (k_adapter_pieces), so that a stage takes them by one bulk copy.
+__host__ __device__ inline int64_t max_subs(int64_t T, int64_t count) { return T / SUB + (count < T ? count : T) + 1; }
+__host__ __device__ inline int u_bytes(int r16) { return 3 * r16 * 128; }    // of SUB tokens
+
+// One CTA per SUB tokens of an adapter and matrix u (blockIdx.y).
+struct PiecesArgs {
+  const float* u[2];
+  uint8_t* out[2];
+  int T, r, count;
+};
+__global__ void __launch_bounds__(128) k_adapter_pieces(const __grid_constant__ PiecesArgs a, void* plan) {
+  __shared__ int tok[SUB];
+  pdl_wait_then_release();
+  const PlanView pv = plan_view(plan, a.T, a.count);
+  const int k = blockIdx.x / (CHUNK / SUB), sub = blockIdx.x % (CHUNK / SUB);
+  if (!plan_ok(pv, a.T, a.count) || k >= pv.head[H_CHUNKS]) return;
+  const int4 chunk = pv.chunks[k];
+  const int first = chunk.y + sub * SUB, cnt = min(SUB, pv.start[chunk.x + 1] - first), r16 = (a.r + 15) / 16 * 16;
+  if (cnt <= 0) return;
+  if (threadIdx.x < SUB) tok[threadIdx.x] = threadIdx.x < cnt ? pv.order[first + threadIdx.x] : -1;
+  __syncthreads();
+  const float* u = a.u[blockIdx.y];
+  uint8_t* out = a.out[blockIdx.y] + (int64_t)(chunk.w + sub) * u_bytes(r16);
+  for (int e = threadIdx.x; e < r16 * (SUB / 8); e += 128) {
+    const int j = e % r16, o = e / r16;
+    float f[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int t = tok[8 * o + q];
+      f[q] = t >= 0 && j < a.r ? u[(int64_t)t * a.r + j] : 0.f;
+    }
+    store_pieces<3>(out + j * 128 + ((o ^ (j & 7)) << 4), r16 * 128, f);
+  }
 }
-template <typename TX, int RB>
-__global__ void __launch_bounds__(TT, 2) k_adapter_outer_tc(const __grid_constant__ OuterArgs<TX> a, void* plan) {
-  constexpr int PX = pieces<TX>(), XB = 64 * 256;        // bytes of one piece of 64 tokens x 128 columns
+
+template <typename TX>
+__host__ __device__ inline int outer_stage(int r16) { return SUB * 256 * pieces<TX>() + u_bytes(r16); }
+// two CTAs on an SM where two stages of each fit
+__host__ __device__ inline int outer_stages(int stage) {
+  const int s = (stage <= 55 * 1024 ? 110 * 1024 : 220 * 1024) / stage;
+  return s > 4 ? 4 : s;
+}
+template <typename TX>
+struct OuterPair {             // column blocks [0, split) are the first's, the rest the second's
+  OuterArgs<TX> a[2];
+  const uint8_t* u[2];
+  int split;
+};
+template <typename TX, bool CP>
+__global__ void __launch_bounds__(ST, 2) k_adapter_outer_tc(const __grid_constant__ OuterPair<TX> both, void* plan) {
+  constexpr int PX = pieces<TX>(), XB = SUB * 256;       // bytes of one piece of SUB tokens x 128 columns
   extern __shared__ uint8_t smem_raw[];
   __shared__ int tok[CHUNK];
-  __shared__ uint64_t bars[2];
+  __shared__ uint64_t full[4], empty[4], all_done;
   __shared__ uint32_t tmem_base;
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int which = (int)blockIdx.x >= both.split;
+  const OuterArgs<TX>& a = both.a[which];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait_then_release();
   const PlanView pv = plan_view(plan, a.T, a.count);
   if (!plan_ok(pv, a.T, a.count) || (int)blockIdx.y >= pv.head[H_CHUNKS]) return;
   const int4 chunk = pv.chunks[blockIdx.y];
   const int l = chunk.x, cnt = max(0, min(CHUNK, pv.start[l + 1] - chunk.y)), r = a.r;
-  const int c0 = blockIdx.x * 128, r16 = (r + 15) / 16 * 16;
-  for (int i = tid; i < CHUNK; i += TT) tok[i] = i < cnt ? pv.order[chunk.y + i] : -1;
+  const int c0 = ((int)blockIdx.x - (which ? both.split : 0)) * 128, r16 = (r + 15) / 16 * 16;
+  for (int i = tid; i < CHUNK; i += ST) tok[i] = i < cnt ? pv.order[chunk.y + i] : -1;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int stage = PX * XB + 3 * r16 * 128;
+  const int stage = outer_stage<TX>(r16), stages = outer_stages(stage);
   if (tid == 0) {
-    mbar_init(&bars[0], 1);
-    mbar_init(&bars[1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&full[i], 3), mbar_init(&empty[i], 1);
+    mbar_init(&all_done, 1);
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&tmem_base, TC_COLS);
@@ -1152,50 +1199,51 @@ __global__ void __launch_bounds__(TT, 2) k_adapter_outer_tc(const __grid_constan
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   bool ok = true;
-  const int accs = tc_accs(r16), mains = accs - 1, steps = (cnt + 63) / 64;
-  Eight<TX> xr[64 * 16 / TT];
-  float ur[RB * 8 / TT][8];
-  auto load = [&](int i) {
-    const int c = c0 + 8 * (tid % 16), left = a.width - c;
+  const int accs = tc_accs(r16), mains = accs - 1, steps = (cnt + SUB - 1) / SUB;
+  if (warp < 8) {
+    const int s = warp / 2;
+    if (s < stages) {
+      const int ch = lane % 16, row0 = lane / 16 + 2 * (warp % 2), c = c0 + 8 * ch, left = a.width - c;
+      uint8_t* xs = sm + s * stage;
+      auto spot = [&](int row) { return (ch / 8) * 8192 + row * 128 + (((ch % 8) ^ (row & 7)) << 4); };
+      for (int i = s; i < steps; i += stages) {
+        if (i >= stages) ok = ok && mbar_wait(&empty[s], (uint32_t)((i / stages - 1) & 1));
+        if (warp % 2 == 0 && lane == 0) {
+          mbar_arrive_expect_tx(&full[s], (uint32_t)u_bytes(r16));
+          bulk_load_1d(xs + PX * XB, both.u[which] + (int64_t)(chunk.w + i) * u_bytes(r16), (uint32_t)u_bytes(r16), &full[s]);
+        }
+        // rows past the adapter's tokens are 0: they would meet u's zeros as anything
+        if constexpr (CP) {
 #pragma unroll
-    for (int k = 0; k < 64 * 16 / TT; ++k) {
-      const int t = tok[64 * i + tid / 16 + k * (TT / 16)];
-      xr[k].zero();
-      if (t >= 0 && left > 0) xr[k].load(a.x + (int64_t)t * a.ldx + c, a.vec_x, left);
-    }
-#pragma unroll
-    for (int k = 0; k < RB * 8 / TT; ++k) {
-      const int e = tid + k * TT, j = e % r16, o = e / r16;          // rank j of tokens 8 o ..
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int t = o < 8 ? tok[64 * i + 8 * o + q] : -1;
-        ur[k][q] = t >= 0 && j < r ? __ldg(a.u + (int64_t)t * r + j) : 0.f;
+          for (int k = 0; k < SUB / 4; ++k) {
+            const int row = row0 + 4 * k, t = tok[SUB * i + row];
+            const bool there = t >= 0 && left > 0;
+            cp16(xs + spot(row), a.x + (there ? (int64_t)t * a.ldx + c : 0), there);
+          }
+          cp_wait_all();
+        } else {
+#pragma unroll 4
+          for (int k = 0; k < SUB / 4; ++k) {
+            const int row = row0 + 4 * k, t = tok[SUB * i + row];
+            Eight<TX> v;
+            v.zero();
+            if (t >= 0 && left > 0) v.load(a.x + (int64_t)t * a.ldx + c, a.vec_x, left);
+            v.store(xs + spot(row), XB);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
       }
     }
-  };
-  if (steps > 0) load(0);
-  const uint32_t idesc = make_idesc_bf16(128, r16, 1, 0);
-  for (int i = 0; i < steps; ++i) {
-    const int s = i & 1;
-    if (i >= 2) ok = ok && mbar_wait(&bars[s], (uint32_t)(((i >> 1) - 1) & 1));
-    uint8_t* xs = sm + s * stage;
-    uint8_t* us = xs + PX * XB;
-    const int ch = tid % 16;
-#pragma unroll
-    for (int k = 0; k < 64 * 16 / TT; ++k) {
-      const int row = tid / 16 + k * (TT / 16);
-      xr[k].store(xs + (ch / 8) * 8192 + row * 128 + (((ch % 8) ^ (row & 7)) << 4), XB);
-    }
-#pragma unroll
-    for (int k = 0; k < RB * 8 / TT; ++k) {
-      const int e = tid + k * TT, j = e % r16, o = e / r16;
-      if (o < 8) store_pieces<3>(us + j * 128 + ((o ^ (j & 7)) << 4), r16 * 128, ur[k]);
-    }
-    if (i + 1 < steps) load(i + 1);
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0 && ok) {
-      const uint32_t xa = smem_u32(xs), ua = smem_u32(us);
+  } else if (lane == 0) {
+    const uint32_t idesc = make_idesc_bf16(128, r16, 1, 0);
+    for (int i = 0; i < steps; ++i) {
+      const int s = i % stages;
+      ok = mbar_wait(&full[s], (uint32_t)((i / stages) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t xa = smem_u32(sm + s * stage), ua = xa + PX * XB;
       bool small = i > 0;
 #pragma unroll
       for (int px = 0; px < PX; ++px)
@@ -1210,14 +1258,12 @@ __global__ void __launch_bounds__(TT, 2) k_adapter_outer_tc(const __grid_constan
                        (main ? i >= mains : small) || kk > 0);
           if (!main) small = true;
         }
-      tc_commit(&bars[s]);
+      tc_commit(&empty[s]);
     }
+    if (steps > 0 && ok) tc_commit(&all_done);
   }
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int used = (steps + 1 - s) / 2;
-    if (used > 0) ok = ok && mbar_wait(&bars[s], (uint32_t)((used - 1) & 1));
-  }
+  __syncwarp();
+  if (steps > 0) ok = ok && mbar_wait(&all_done, 0u);
   __syncwarp();
   tc_fence_after();
   const int c = c0 + tid;

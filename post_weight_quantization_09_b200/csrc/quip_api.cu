@@ -1896,7 +1896,8 @@ bool regions_overlap(const void* a, int64_t lda, int64_t cols_a, size_t size_a, 
 }
 
 struct AdapterWs {
-  size_t plan = 0, h = 0, part_down = 0, part_up = 0, total = 0;   // offsets
+  size_t plan = 0, h = 0, part_down = 0, part_up = 0, pieces = 0, total = 0;   // offsets
+  size_t pieces_each = 0;                    // bytes of one matrix's pieces
 };
 AdapterWs adapter_ws(int64_t T, int64_t n, int64_t m, int64_t r, int64_t count, bool backward) {
   AdapterWs w;
@@ -1907,6 +1908,11 @@ AdapterWs adapter_ws(int64_t T, int64_t n, int64_t m, int64_t r, int64_t count, 
     w.total += round256((size_t)ad::max_slots(T) * r * n * 4);
     w.part_up = w.total;
     w.total += round256((size_t)ad::max_slots(T) * r * m * 4);
+    if (r <= 128) {
+      w.pieces = w.total;
+      w.pieces_each = round256((size_t)ad::max_subs(T, count) * ad::u_bytes((int)(r + 15) / 16 * 16));
+      w.total += 2 * w.pieces_each;
+    }
   }
   return w;
 }
@@ -2060,30 +2066,82 @@ cudaError_t adapter_dispatch(int x_dtype, int w_dtype, int y_dtype, const Adapte
   }
 }
 
-template <int RB, typename TX>
-cudaError_t adapter_outer_tc(const ad::OuterArgs<TX>& a, void* plan, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  auto* kernel = ad::k_adapter_outer_tc<TX, RB>;
-  cudaError_t e = allow_smem(kernel, ad::outer_smem<TX>(RB), done);
-  if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((a.width + 127) / 128), (unsigned)ad::max_tiles(a.T, a.count, ad::CHUNK));
-  LaunchScope ls("k_adapter_outer_tc", st);
-  return launch_pdl(kernel, grid, dim3(ad::TT), ad::outer_smem<TX>((a.r + 15) / 16 * 16), st, a, plan);
-}
-
+// The weight gradients (sums over an adapter's tokens) that are asked for:
+// [0] d_down of (x, dh), [1] d_up of (dy, h).
+struct AdapterSums {
+  const void* x[2];
+  int64_t ldx[2], width[2];
+  int dtype[2];
+  const float* u[2];
+  const float* scale[2];
+  float *out[2], *partial[2];
+  uint8_t* pieces[2];
+  int64_t T, r, count;
+  int accumulate;
+};
 template <typename TX>
-cudaError_t adapter_outer(const void* x, int64_t ldx, const float* u, const float* scale, float* out, float* partial,
-                          int64_t T, int64_t width, int64_t r, int64_t count, int accumulate, void* plan,
-                          cudaStream_t st) {
-  ad::OuterArgs<TX> a{static_cast<const TX*>(x), ldx, u, scale, out, partial, (int)T, (int)width, (int)r,
-                      (int)count, accumulate, rows_of_eight(x, T > 1 ? ldx : 8, sizeof(TX))};
-  if (r <= 64) return adapter_outer_tc<64>(a, plan, st);
-  if (r <= 128) return adapter_outer_tc<128>(a, plan, st);
-  a.vec_x = rows_of_four(x, T > 1 ? ldx : 4, sizeof(TX));
-  const dim3 grid((unsigned)((width + 4 * ad::OT - 1) / (4 * ad::OT)), (unsigned)((r + ad::OROWS - 1) / ad::OROWS),
-                  (unsigned)ad::max_tiles(T, count, ad::CHUNK));
-  LaunchScope ls("k_adapter_outer", st);
-  return launch_pdl(ad::k_adapter_outer<TX>, grid, dim3(ad::OT), 0, st, a, plan);
+ad::OuterArgs<TX> outer_args(const AdapterSums& s, int k) {
+  return {static_cast<const TX*>(s.x[k]), s.ldx[k], s.u[k], s.scale[k], s.out[k], s.partial[k], (int)s.T,
+          (int)s.width[k], (int)s.r, (int)s.count, s.accumulate,
+          rows_of_eight(s.x[k], s.T > 1 ? s.ldx[k] : 8, sizeof(TX))};
+}
+// One launch for sum k, or for both.
+template <typename TX, bool CP>
+cudaError_t adapter_outer_tc(const AdapterSums& s, int k, bool both, void* plan, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  auto* kernel = ad::k_adapter_outer_tc<TX, CP>;
+  cudaError_t e = allow_smem(kernel, 222 * 1024, done);
+  if (e != cudaSuccess) return e;
+  const int64_t b0 = (s.width[k] + 127) / 128, b1 = both ? (s.width[1] + 127) / 128 : 0;
+  const ad::OuterPair<TX> pair{{outer_args<TX>(s, k), outer_args<TX>(s, both ? 1 : k)},
+                               {s.pieces[k], s.pieces[both ? 1 : k]}, (int)b0};
+  const int stage = ad::outer_stage<TX>((int)(s.r + 15) / 16 * 16);
+  LaunchScope ls("k_adapter_outer_tc", st);
+  return launch_pdl(kernel, dim3((unsigned)(b0 + b1), (unsigned)ad::max_tiles(s.T, s.count, ad::CHUNK)), dim3(ad::ST),
+                    (size_t)ad::outer_stages(stage) * stage + 1024, st, pair, plan);
+}
+template <typename TX>
+cudaError_t adapter_outer(const AdapterSums& s, int k, bool both, void* plan, cudaStream_t st) {
+  if (s.r <= 128) {
+    const bool vec = rows_of_eight(s.x[k], s.T > 1 ? s.ldx[k] : 8, sizeof(TX)) &&
+                     (!both || rows_of_eight(s.x[1], s.T > 1 ? s.ldx[1] : 8, sizeof(TX)));
+    if constexpr (sizeof(TX) == 2)
+      if (vec) return adapter_outer_tc<TX, true>(s, k, both, plan, st);
+    return adapter_outer_tc<TX, false>(s, k, both, plan, st);
+  }
+  ad::OuterArgs<TX> a = outer_args<TX>(s, k);
+  a.vec_x = rows_of_four(s.x[k], s.T > 1 ? s.ldx[k] : 4, sizeof(TX));
+  const dim3 grid((unsigned)((s.width[k] + 4 * ad::OT - 1) / (4 * ad::OT)), (unsigned)((s.r + ad::OROWS - 1) / ad::OROWS),
+                  (unsigned)ad::max_tiles(s.T, s.count, ad::CHUNK));
+  {
+    LaunchScope ls("k_adapter_outer", st);
+    cudaError_t e = launch_pdl(ad::k_adapter_outer<TX>, grid, dim3(ad::OT), 0, st, a, plan);
+    if (e != cudaSuccess || !both) return e;
+  }
+  return adapter_outer<TX>(s, 1, false, plan, st);
+}
+cudaError_t adapter_sums(const AdapterSums& s, void* plan, cudaStream_t st) {
+  const bool want[2] = {s.out[0] != nullptr, s.out[1] != nullptr};
+  if (s.r <= 128 && s.T > 0) {
+    const int first = want[0] ? 0 : 1, n = (want[0] ? 1 : 0) + (want[1] ? 1 : 0);
+    const ad::PiecesArgs p{{s.u[first], s.u[1]}, {s.pieces[first], s.pieces[1]}, (int)s.T, (int)s.r, (int)s.count};
+    LaunchScope ls("k_adapter_pieces", st);
+    cudaError_t e = launch_pdl(ad::k_adapter_pieces,
+                               dim3((unsigned)(ad::max_tiles(s.T, s.count, ad::CHUNK) * (ad::CHUNK / ad::SUB)), (unsigned)n),
+                               dim3(128), 0, st, p, plan);
+    if (e != cudaSuccess) return e;
+  }
+  auto one = [&](int k, bool both) {
+    return s.dtype[k] == QUIP_BF16 ? adapter_outer<__nv_bfloat16>(s, k, both, plan, st)
+                                   : adapter_outer<float>(s, k, both, plan, st);
+  };
+  if (want[0] && want[1] && s.dtype[0] == s.dtype[1]) return one(0, true);
+  for (int k = 0; k < 2; ++k)
+    if (want[k]) {
+      cudaError_t e = one(k, false);
+      if (e != cudaSuccess) return e;
+    }
+  return cudaSuccess;
 }
 }  // namespace
 
@@ -2188,14 +2246,12 @@ quip_status quip_adapter_backward(const void* x, int x_dtype, int64_t ldx, const
                         T, m, n, r, count, true};
     QCHECK(adapter_dispatch(dy_dtype, w_dtype, x_dtype, c, ids, T <= kAdapterDirect ? nullptr : pl, st));
   }
-  if (d_down)
-    QCHECK(x_dtype == QUIP_BF16
-               ? adapter_outer<__nv_bfloat16>(x, ldx, dh, nullptr, d_down, part_down, T, n, r, count, accumulate, pl, st)
-               : adapter_outer<float>(x, ldx, dh, nullptr, d_down, part_down, T, n, r, count, accumulate, pl, st));
-  if (d_up)
-    QCHECK(dy_dtype == QUIP_BF16
-               ? adapter_outer<__nv_bfloat16>(dy, lddy, h, scale, d_up, part_up, T, m, r, count, accumulate, pl, st)
-               : adapter_outer<float>(dy, lddy, h, scale, d_up, part_up, T, m, r, count, accumulate, pl, st));
+  if (d_down || d_up) {
+    uint8_t* pieces = reinterpret_cast<uint8_t*>(w8 + w.pieces);
+    const AdapterSums sums{{x, dy}, {ldx, lddy}, {n, m}, {x_dtype, dy_dtype}, {dh, h}, {nullptr, scale}, {d_down, d_up},
+                           {part_down, part_up}, {pieces, pieces + w.pieces_each}, T, r, count, accumulate};
+    QCHECK(adapter_sums(sums, pl, st));
+  }
   if ((d_down || d_up) && T > ad::CHUNK) {
     const int64_t s0 = d_down ? r * n : 0, s1 = d_up ? r * m : 0;
     const unsigned gx = (unsigned)std::min<int64_t>((s0 + s1 + 255) / 256, 4 * num_sms());
