@@ -39,7 +39,7 @@ constexpr int MAX_RANK = QUIP_ADAPTER_MAX_RANK;
 //           -1 for an adapter's only chunk, else its place among the partial
 //           sums; sub: the number of its first SUB tokens among all runs of SUB
 //   parts   (first slot, number of slots) per adapter, 0 slots with one chunk
-constexpr int HEAD = 16, TILE = 128, SMALL = 8, CHUNK = 512, SUB = 64;
+constexpr int HEAD = 16, TILE = 128, SMALL = 8, CHUNK = 1024, SUB = 64;
 enum { H_MAGIC, H_T, H_COUNT, H_TILES, H_SMALL, H_CHUNKS, H_BAD };
 constexpr int MAGIC = 0x51AD;
 
@@ -125,11 +125,18 @@ __global__ void __launch_bounds__(PLAN_WARPS * 32)
     if (b >= count && report) record_status(QUIP_ERR_ARG);
     return b < 0 || b >= count ? count : b;
   };
-  for (int t = t0; t < t1; t += 32) {
-    const int b = t + lane < t1 ? bucket(t + lane, true) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, b);
-    if (b >= 0 && lane == __ffs(same) - 1) mine[b] += __popc(same);
-    __syncwarp();
+  constexpr int AHEAD = 8;                     // rounds whose ids are loaded together
+  for (int t = t0; t < t1; t += 32 * AHEAD) {
+    int b[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) b[k] = t + 32 * k + lane < t1 ? bucket(t + 32 * k + lane, true) : -1;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (t + 32 * k >= t1) break;
+      const unsigned same = __match_any_sync(0xffffffffu, b[k]);
+      if (b[k] >= 0 && lane == __ffs(same) - 1) mine[b[k]] += __popc(same);
+      __syncwarp();
+    }
   }
   __syncthreads();
   // per bucket: the warps' counts to offsets within it
@@ -173,13 +180,19 @@ __global__ void __launch_bounds__(PLAN_WARPS * 32)
     pv.head[H_CHUNKS] = nchunk;
   }
   __syncthreads();
-  for (int t = t0; t < t1; t += 32) {
-    const int b = t + lane < t1 ? bucket(t + lane, false) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, b);
-    if (b >= 0) pv.order[mine[b] + __popc(same & ((1u << lane) - 1u))] = t + lane;
-    __syncwarp();
-    if (b >= 0 && lane == __ffs(same) - 1) mine[b] += __popc(same);
-    __syncwarp();
+  for (int t = t0; t < t1; t += 32 * AHEAD) {
+    int b[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) b[k] = t + 32 * k + lane < t1 ? bucket(t + 32 * k + lane, false) : -1;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (t + 32 * k >= t1) break;
+      const unsigned same = __match_any_sync(0xffffffffu, b[k]);
+      if (b[k] >= 0) pv.order[mine[b[k]] + __popc(same & ((1u << lane) - 1u))] = t + 32 * k + lane;
+      __syncwarp();
+      if (b[k] >= 0 && lane == __ffs(same) - 1) mine[b[k]] += __popc(same);
+      __syncwarp();
+    }
   }
   // the tables, a warp per adapter: thread l's numbers go through shared memory
   __syncthreads();
@@ -490,7 +503,10 @@ constexpr int XT_BYTES = TILE * 128;           // one piece of 128 tokens x 64 c
 
 template <typename TX, typename TW>
 __host__ __device__ inline int shrink_stage(int r16) { return pieces<TX>() * XT_BYTES + pieces<TW>() * r16 * 128; }
-constexpr int ST = 288;                        // threads: four pairs of warps with a stage each, a warp to multiply
+// Warps per stage (four where registers are between), and threads: four stages
+// and a warp to multiply.
+template <bool CP> __host__ __device__ constexpr int stage_warps() { return CP ? 2 : 4; }
+template <bool CP> __host__ __device__ constexpr int stage_threads() { return 32 * (4 * stage_warps<CP>() + 1); }
 __host__ __device__ inline int shrink_stages(int stage) { return stage <= 24 * 1024 ? 4 : 3; }
 template <typename TX, typename TW>
 __host__ __device__ inline int shrink_smem(int r16) {
@@ -587,9 +603,9 @@ template <> struct Eight<float> {
 __host__ __device__ constexpr int tc_accs(int r16) { return r16 <= 64 ? 4 : 2; }
 
 template <typename TX, typename TW, bool CP>
-__global__ void __launch_bounds__(ST, 2)
+__global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
     k_adapter_shrink(const __grid_constant__ ApplyArgs<TX, TW, float> a, void* plan) {
-  constexpr int PX = pieces<TX>(), PW = pieces<TW>();
+  constexpr int PX = pieces<TX>(), PW = pieces<TW>(), SW = stage_warps<CP>(), ST = stage_threads<CP>();
   constexpr bool SPLIT = PX > 1 || PW > 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int tok[TILE];
@@ -613,7 +629,7 @@ __global__ void __launch_bounds__(ST, 2)
   const int r16 = (r + 15) / 16 * 16, stage = shrink_stage<TX, TW>(r16), stages = shrink_stages(stage);
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&full[i], 2), mbar_init(&empty[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&full[i], SW), mbar_init(&empty[i], 1);
     mbar_init(&all_done, 1);
     fence_mbar_init();
   }
@@ -628,10 +644,10 @@ __global__ void __launch_bounds__(ST, 2)
   const int blocks = (a.n + 63) / 64, per = (blocks + nc - 1) / nc;
   const int k0 = min(blocks, rank * per), steps = min(blocks, k0 + per) - k0;
   const int accs = tc_accs(r16), mains = SPLIT ? accs - 1 : accs;
-  if (warp < 8) {
-    const int s = warp / 2;
+  if (warp < 4 * SW) {
+    const int s = warp / SW;
     if (s < stages) {
-      const int ch = lane % 8, row0 = lane / 8 + 4 * (warp % 2);   // the lane's 16-byte column and first row
+      const int ch = lane % 8, row0 = lane / 8 + 4 * (warp % SW);   // the lane's 16-byte column and first row
       uint8_t* xs = sm + s * stage;
       uint8_t* ps = xs + PX * XT_BYTES;
       auto spot = [&](int row) { return row * 128 + ((ch ^ (row & 7)) << 4); };
@@ -641,24 +657,24 @@ __global__ void __launch_bounds__(ST, 2)
         if constexpr (CP) {
           const __nv_bfloat16* x = a.x + (c < a.n ? c : 0);
 #pragma unroll 8
-          for (int row = row0; row < cnt; row += 8)    // rows past the tile's tokens only feed their own sums
+          for (int row = row0; row < cnt; row += 4 * SW)    // rows past the tile's tokens only feed their own sums
             cp16(xs + spot(row), x + (int64_t)tok[row] * a.ldx, c < a.n);
 #pragma unroll 4
-          for (int row = row0; row < r16; row += 8) {
+          for (int row = row0; row < r16; row += 4 * SW) {
             const bool there = row < r && c < a.n;
             cp16(ps + spot(row), P + (there ? (int64_t)row * a.n + c : 0), there);
           }
           cp_wait_all();
         } else {
 #pragma unroll 4
-          for (int row = row0; row < cnt; row += 8) {
+          for (int row = row0; row < cnt; row += 4 * SW) {
             Eight<TX> v;
             v.zero();
             if (left > 0) v.load(a.x + (int64_t)tok[row] * a.ldx + c, a.vec_x, left);
             v.store(xs + spot(row), XT_BYTES);
           }
 #pragma unroll 4
-          for (int row = row0; row < r16; row += 8) {
+          for (int row = row0; row < r16; row += 4 * SW) {
             Eight<TW> v;
             v.zero();
             if (row < r && left > 0) v.load(P + (int64_t)row * a.n + c, a.vec_p, left);
@@ -1115,12 +1131,12 @@ __global__ void __launch_bounds__(OT) k_adapter_outer(const __grid_constant__ Ou
       }
 }
 
-// The same on the tensor cores, 128 columns and all ranks (up to 128) per
-// CTA: D[column][j] = x^T u (M = 128 columns, N = r, K = tokens, x MN-major as
-// its rows lie in memory), SUB tokens at a time.  u is cut into three bf16
-// pieces; the large terms are dealt out over all accumulators but one, which
-// takes the small ones, so few steps meet in each (tc_accs).  The pieces are
-// made once, K-major and swizzled as the tensor core reads them
+// The same on the tensor cores: D[column][j] = x^T u (M = 128 columns, N = r,
+// K = tokens, x MN-major as its rows lie in memory), SUB tokens at a time, two
+// times 128 columns (one with fp32 rows) that share u's tile.  u is cut into
+// three bf16 pieces; the large terms are dealt out over all accumulators but
+// one, which takes the small ones, so few steps meet in each (tc_accs).  The
+// pieces are made once, K-major and swizzled as the tensor core reads them
 // (k_adapter_pieces), so that a stage takes them by one bulk copy.
 __host__ __device__ inline int64_t max_subs(int64_t T, int64_t count) { return T / SUB + (count < T ? count : T) + 1; }
 __host__ __device__ inline int u_bytes(int r16) { return 3 * r16 * 128; }    // of SUB tokens
@@ -1156,11 +1172,14 @@ __global__ void __launch_bounds__(128) k_adapter_pieces(const __grid_constant__ 
   }
 }
 
+// Halves of 128 columns per CTA.
+template <typename TX> __host__ __device__ constexpr int outer_halves() { return sizeof(TX) == 2 ? 2 : 1; }
 template <typename TX>
-__host__ __device__ inline int outer_stage(int r16) { return SUB * 256 * pieces<TX>() + u_bytes(r16); }
-// two CTAs on an SM where two stages of each fit
+__host__ __device__ inline int outer_stage(int r16) {
+  return SUB * 256 * pieces<TX>() * outer_halves<TX>() + u_bytes(r16);
+}
 __host__ __device__ inline int outer_stages(int stage) {
-  const int s = (stage <= 55 * 1024 ? 110 * 1024 : 220 * 1024) / stage;
+  const int s = 216 * 1024 / stage;
   return s > 4 ? 4 : s;
 }
 template <typename TX>
@@ -1169,137 +1188,182 @@ struct OuterPair {             // column blocks [0, split) are the first's, the 
   const uint8_t* u[2];
   int split;
 };
+// Resident CTAs, each an equal run of the (column block, chunk) pairs, the
+// chunks inside, so that long and short ones mix.  Warps: the stages', one to
+// multiply, others that write a pair's sums while the next is multiplied into
+// the other half of TMEM (where two sets of accumulators fit); each goes
+// through the pairs by itself.
 template <typename TX, bool CP>
-__global__ void __launch_bounds__(ST, 2) k_adapter_outer_tc(const __grid_constant__ OuterPair<TX> both, void* plan) {
+__host__ __device__ constexpr int outer_threads() { return stage_threads<CP>() + 128 * outer_halves<TX>(); }
+template <typename TX, bool CP>
+__global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
+    k_adapter_outer_tc(const __grid_constant__ OuterPair<TX> both, int blocks, void* plan) {
   constexpr int PX = pieces<TX>(), XB = SUB * 256;       // bytes of one piece of SUB tokens x 128 columns
+  constexpr int SW = stage_warps<CP>(), MW = 4 * SW, H = outer_halves<TX>();
+  constexpr int CHS = 16 * H, ROWS = SUB / SW, AT_ONCE = 32 / CHS, TCOLS = TC_COLS * H;   // 16-byte columns; a warp's rows
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int tok[CHUNK];
-  __shared__ uint64_t full[4], empty[4], all_done;
+  __shared__ uint64_t full[4], empty[4], ready[2], drained[2];
   __shared__ uint32_t tmem_base;
-  const int which = (int)blockIdx.x >= both.split;
-  const OuterArgs<TX>& a = both.a[which];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait_then_release();
-  const PlanView pv = plan_view(plan, a.T, a.count);
-  if (!plan_ok(pv, a.T, a.count) || (int)blockIdx.y >= pv.head[H_CHUNKS]) return;
-  const int4 chunk = pv.chunks[blockIdx.y];
-  const int l = chunk.x, cnt = max(0, min(CHUNK, pv.start[l + 1] - chunk.y)), r = a.r;
-  const int c0 = ((int)blockIdx.x - (which ? both.split : 0)) * 128, r16 = (r + 15) / 16 * 16;
-  for (int i = tid; i < CHUNK; i += ST) tok[i] = i < cnt ? pv.order[chunk.y + i] : -1;
+  const int T = both.a[0].T, count = both.a[0].count, r = both.a[0].r;
+  const PlanView pv = plan_view(plan, T, count);
+  if (!plan_ok(pv, T, count)) return;
+  const int chunks = pv.head[H_CHUNKS];
+  const int64_t work = (int64_t)chunks * blocks;
+  const int64_t w0 = work * blockIdx.x / gridDim.x, w1 = work * (blockIdx.x + 1) / gridDim.x;
+  if (w0 == w1) return;
+  const int r16 = (r + 15) / 16 * 16, accs = tc_accs(r16), mains = accs - 1;
+  const int sets = 2 * H * accs * r16 <= TCOLS ? 2 : 1;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int stage = outer_stage<TX>(r16), stages = outer_stages(stage);
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&full[i], 3), mbar_init(&empty[i], 1);
-    mbar_init(&all_done, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&full[i], 1 + SW), mbar_init(&empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ready[i], 1), mbar_init(&drained[i], 4 * H);
     fence_mbar_init();
   }
-  if (warp == 0) tmem_alloc(&tmem_base, TC_COLS);
+  if (warp == 0) tmem_alloc(&tmem_base, TCOLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   bool ok = true;
-  const int accs = tc_accs(r16), mains = accs - 1, steps = (cnt + SUB - 1) / SUB;
-  if (warp < 8) {
-    const int s = warp / 2;
-    if (s < stages) {
-      const int ch = lane % 16, row0 = lane / 16 + 2 * (warp % 2), c = c0 + 8 * ch, left = a.width - c;
-      uint8_t* xs = sm + s * stage;
-      auto spot = [&](int row) { return (ch / 8) * 8192 + row * 128 + (((ch % 8) ^ (row & 7)) << 4); };
-      for (int i = s; i < steps; i += stages) {
-        if (i >= stages) ok = ok && mbar_wait(&empty[s], (uint32_t)((i / stages - 1) & 1));
-        if (warp % 2 == 0 && lane == 0) {
-          mbar_arrive_expect_tx(&full[s], (uint32_t)u_bytes(r16));
-          bulk_load_1d(xs + PX * XB, both.u[which] + (int64_t)(chunk.w + i) * u_bytes(r16), (uint32_t)u_bytes(r16), &full[s]);
-        }
-        // rows past the adapter's tokens are 0: they would meet u's zeros as anything
-        if constexpr (CP) {
-#pragma unroll
-          for (int k = 0; k < SUB / 4; ++k) {
-            const int row = row0 + 4 * k, t = tok[SUB * i + row];
-            const bool there = t >= 0 && left > 0;
-            cp16(xs + spot(row), a.x + (there ? (int64_t)t * a.ldx + c : 0), there);
+  // pair w's chunk and its number of tokens, looked up one pair ahead
+  auto look = [&](int64_t w, int4& chunk, int& cnt) {
+    if (w < w1) {
+      chunk = pv.chunks[w % chunks];
+      cnt = max(0, min(CHUNK, pv.start[chunk.x + 1] - chunk.y));
+    }
+  };
+  int4 chunk, next;
+  int cnt, next_cnt;
+  look(w0, chunk, cnt);
+  int fills = 0, items = 0;                    // stages filled and pairs with tokens before this one
+  for (int64_t w = w0; w < w1; ++w, chunk = next, cnt = next_cnt) {
+    look(w + 1, next, next_cnt);
+    const int l = chunk.x, steps = (cnt + SUB - 1) / SUB, block = (int)(w / chunks), which = block >= both.split;
+    const OuterArgs<TX>& a = both.a[which];
+    const int c0 = (block - (which ? both.split : 0)) * 128 * H;
+    if (warp < MW) {
+      const int s = warp / SW;
+      if (s < stages) {
+        // stage s takes fills f = s modulo the stages
+        const int ch = lane % CHS, row0 = ROWS * (warp % SW), c = c0 + 8 * ch, left = a.width - c;
+        uint8_t* xs = sm + s * stage;
+        auto spot = [&](int row) { return (ch / 8) * 8192 + row * 128 + (((ch % 8) ^ (row & 7)) << 4); };
+        for (int i = ((s - fills) % stages + stages) % stages; i < steps; i += stages) {
+          const int f = fills + i, rows = min(ROWS, cnt - SUB * i - row0);       // of this warp's that are there
+          const int mine = lane < rows ? pv.order[chunk.y + SUB * i + row0 + lane] : -1;
+          if (f >= stages) ok = ok && mbar_wait(&empty[s], (uint32_t)((f / stages - 1) & 1));
+          __syncwarp();
+          if (warp % SW == 0 && lane == 0) {
+            mbar_arrive_expect_tx(&full[s], (uint32_t)u_bytes(r16));
+            bulk_load_1d(xs + PX * H * XB, both.u[which] + (int64_t)(chunk.w + i) * u_bytes(r16), (uint32_t)u_bytes(r16),
+                         &full[s]);
           }
-          cp_wait_all();
-        } else {
+          // rows past the adapter's tokens are 0: they would meet u's zeros as anything
+          if constexpr (CP) {
+#pragma unroll 8
+            for (int k = 0; k < ROWS; k += AT_ONCE) {
+              const int row = k + lane / CHS, t = __shfl_sync(0xffffffffu, mine, row);
+              const bool there = t >= 0 && left > 0;
+              cp16(xs + spot(row0 + row), a.x + (there ? (int64_t)t * a.ldx + c : 0), there);
+            }
+            cp_wait_all();
+          } else {
 #pragma unroll 4
-          for (int k = 0; k < SUB / 4; ++k) {
-            const int row = row0 + 4 * k, t = tok[SUB * i + row];
-            Eight<TX> v;
-            v.zero();
-            if (t >= 0 && left > 0) v.load(a.x + (int64_t)t * a.ldx + c, a.vec_x, left);
-            v.store(xs + spot(row), XB);
+            for (int k = 0; k < ROWS; k += AT_ONCE) {
+              const int row = k + lane / CHS, t = __shfl_sync(0xffffffffu, mine, row);
+              Eight<TX> v;
+              v.zero();
+              if (t >= 0 && left > 0) v.load(a.x + (int64_t)t * a.ldx + c, a.vec_x, left);
+              v.store(xs + spot(row0 + row), H * XB);
+            }
           }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
-      }
-    }
-  } else if (lane == 0) {
-    const uint32_t idesc = make_idesc_bf16(128, r16, 1, 0);
-    for (int i = 0; i < steps; ++i) {
-      const int s = i % stages;
-      ok = mbar_wait(&full[s], (uint32_t)((i / stages) & 1));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t xa = smem_u32(sm + s * stage), ua = xa + PX * XB;
-      bool small = i > 0;
-#pragma unroll
-      for (int px = 0; px < PX; ++px)
-#pragma unroll
-        for (int pu = 0; pu < 3 - px; ++pu) {
-          const bool main = px + pu == 0;
-          const uint32_t d = tmem + (uint32_t)((main ? i % mains : accs - 1) * r16);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f16(d, make_sw128_desc(xa + px * XB + kk * 2048, 8192, 1024),
-                       make_sw128_desc(ua + pu * r16 * 128 + kk * 32, 16, 1024), idesc,
-                       (main ? i >= mains : small) || kk > 0);
-          if (!main) small = true;
-        }
-      tc_commit(&empty[s]);
-    }
-    if (steps > 0 && ok) tc_commit(&all_done);
-  }
-  __syncwarp();
-  if (steps > 0) ok = ok && mbar_wait(&all_done, 0u);
-  __syncwarp();
-  tc_fence_after();
-  const int c = c0 + tid;
-  if (warp < 4) {
-    const float k = a.scale ? a.scale[l] : 1.f;
-    float* out = chunk.z < 0 ? a.out + (int64_t)l * r * a.width : a.partial + (int64_t)chunk.z * r * a.width;
-    const bool add = chunk.z < 0 && a.accumulate;
-    const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16);
-    for (int j = 0; j < r16; j += 16) {
-      float v[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = 0.f;
-      for (int q = accs - 1; q >= 0; --q) {    // the small terms first
-        if (q == accs - 1 ? steps > 0 : q < steps) {
-          float w[16];
-          tmem_ld16(at + q * r16 + j, w);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] += w[e];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
         }
       }
-      if (c < a.width && ok) {
+    } else if (warp == MW) {
+      if (lane == 0) {
+        const uint32_t idesc = make_idesc_bf16(128, r16, 1, 0);
+        for (int i = 0; i < steps && ok; ++i) {
+          const int f = fills + i, s = f % stages, n = items;
+          if (i == 0 && n >= sets) ok = mbar_wait(&drained[n % sets], (uint32_t)((n / sets - 1) & 1));
+          ok = ok && mbar_wait(&full[s], (uint32_t)((f / stages) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t xa = smem_u32(sm + s * stage), ua = xa + PX * H * XB;
+          const uint32_t set = tmem + (uint32_t)(n % sets * (TCOLS / 2));
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (j + e < r) {
-            float* o = out + (int64_t)(j + e) * a.width + c;
-            *o = (add ? *o : 0.f) + k * v[e];
+          for (int hh = 0; hh < H; ++hh) {
+            bool small = i > 0;
+#pragma unroll
+            for (int px = 0; px < PX; ++px)
+#pragma unroll
+              for (int pu = 0; pu < 3 - px; ++pu) {
+                const bool main = px + pu == 0;
+                const uint32_t d = set + (uint32_t)((hh * accs + (main ? i % mains : accs - 1)) * r16);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma_f16(d, make_sw128_desc(xa + (px * H + hh) * XB + kk * 2048, 8192, 1024),
+                             make_sw128_desc(ua + pu * r16 * 128 + kk * 32, 16, 1024), idesc,
+                             (main ? i >= mains : small) || kk > 0);
+                if (!main) small = true;
+              }
           }
+          tc_commit(&empty[s]);
+          if (i == steps - 1) tc_commit(&ready[n % sets]);
+        }
       }
       __syncwarp();
+    } else {
+      // TMEM lanes 32 (warp % 4) ..: columns of the warp's half of the block
+      const int half = (warp - MW - 1) / 4, n = items, c = c0 + 128 * half + 32 * (warp % 4) + lane;
+      if (steps > 0) ok = ok && mbar_wait(&ready[n % sets], (uint32_t)((n / sets) & 1));
+      tc_fence_after();
+      const float k = a.scale ? a.scale[l] : 1.f;
+      float* out = chunk.z < 0 ? a.out + (int64_t)l * r * a.width : a.partial + (int64_t)chunk.z * r * a.width;
+      const bool add = chunk.z < 0 && a.accumulate;
+      const uint32_t at = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + (uint32_t)(n % sets * (TCOLS / 2) + half * accs * r16);
+      for (int j = 0; j < r16; j += 16) {
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        for (int q = accs - 1; q >= 0; --q) {            // the small terms first
+          if (q == accs - 1 ? steps > 0 : q < steps) {
+            float t[16];
+            tmem_ld16(at + q * r16 + j, t);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] += t[e];
+          }
+        }
+        if (c < a.width && ok) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (j + e < r) {
+              float* o = out + (int64_t)(j + e) * a.width + c;
+              *o = (add ? *o : 0.f) + k * v[e];
+            }
+        }
+        __syncwarp();
+      }
+      if (steps > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&drained[n % sets]);
+      }
     }
+    if (steps > 0) ++items;
+    fills += steps;
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, TC_COLS);
+    tmem_dealloc(tmem, TCOLS);
   }
 }
 

@@ -1955,12 +1955,12 @@ cudaError_t adapter_shrink(const ad::ApplyArgs<TX, TW, float>& a, void* plan, cu
   auto* kernel = ad::k_adapter_shrink<TX, TW, CP>;
   cudaError_t e = allow_smem(kernel, 226 * 1024, done);
   if (e != cudaSuccess) return e;
-  // CTAs per cluster: as many as fill two per SM, each with a few blocks
-  const int64_t likely = (a.T + ad::TILE - 1) / ad::TILE, blocks = (a.n + 63) / 64;
-  unsigned nc = 1;
-  while (nc < 8 && likely * nc < 2 * (int64_t)num_sms() && nc * 2 <= blocks) nc *= 2;
+  // CTAs per cluster: as many as two per SM hold at once with a part-filled
+  // tile per adapter, each with a block at least
+  const int64_t likely = (a.T + ad::TILE - 1) / ad::TILE + std::min<int64_t>(a.count, a.T / 16), blocks = (a.n + 63) / 64;
+  const unsigned nc = (unsigned)std::min<int64_t>(std::min<int64_t>(8, blocks), std::max<int64_t>(1, 2 * num_sms() / likely));
   LaunchScope ls("k_adapter_shrink", st);
-  return launch_cluster(kernel, (unsigned)(ad::max_tiles(a.T, a.count, ad::TILE) * nc), ad::ST,
+  return launch_cluster(kernel, (unsigned)(ad::max_tiles(a.T, a.count, ad::TILE) * nc), ad::stage_threads<CP>(),
                         ad::shrink_smem<TX, TW>((a.r + 15) / 16 * 16), nc, true, st, a, plan);
 }
 
@@ -2092,13 +2092,15 @@ cudaError_t adapter_outer_tc(const AdapterSums& s, int k, bool both, void* plan,
   auto* kernel = ad::k_adapter_outer_tc<TX, CP>;
   cudaError_t e = allow_smem(kernel, 222 * 1024, done);
   if (e != cudaSuccess) return e;
-  const int64_t b0 = (s.width[k] + 127) / 128, b1 = both ? (s.width[1] + 127) / 128 : 0;
+  constexpr int cols = 128 * ad::outer_halves<TX>();
+  const int64_t b0 = (s.width[k] + cols - 1) / cols, b1 = both ? (s.width[1] + cols - 1) / cols : 0;
   const ad::OuterPair<TX> pair{{outer_args<TX>(s, k), outer_args<TX>(s, both ? 1 : k)},
                                {s.pieces[k], s.pieces[both ? 1 : k]}, (int)b0};
   const int stage = ad::outer_stage<TX>((int)(s.r + 15) / 16 * 16);
   LaunchScope ls("k_adapter_outer_tc", st);
-  return launch_pdl(kernel, dim3((unsigned)(b0 + b1), (unsigned)ad::max_tiles(s.T, s.count, ad::CHUNK)), dim3(ad::ST),
-                    (size_t)ad::outer_stages(stage) * stage + 1024, st, pair, plan);
+  const unsigned grid = (unsigned)std::min<int64_t>(num_sms(), (b0 + b1) * ad::max_tiles(s.T, s.count, ad::CHUNK));
+  return launch_pdl(kernel, dim3(grid), dim3(ad::outer_threads<TX, CP>()), (size_t)ad::outer_stages(stage) * stage + 1024, st,
+                    pair, (int)(b0 + b1), plan);
 }
 template <typename TX>
 cudaError_t adapter_outer(const AdapterSums& s, int k, bool both, void* plan, cudaStream_t st) {

@@ -191,8 +191,8 @@ class Case:
                 tol_dd[l] += np.outer(tol_dh[t], mag[0][0][t])
         tol += 4 * U * mag[1][4] + torch.finfo(self.dx.dtype).eps / 2 * (np.abs(dx) + tol)
         assert np.all(np.abs(host(self.dx) - dx) <= tol), np.max(np.abs(host(self.dx) - dx) / tol)
-        # sums over tokens: 512 in a row at most, then one per further chunk
-        k = 512 + 64 + self.T / 512
+        # sums over tokens: 1024 in a row at most, then one per further chunk
+        k = 1024 + 64 + self.T / 1024
         tol_dd += (k + 4) * U * dd_m + 4 * U * abs(self.acc) + 1e-30
         tol_du = (k + 4) * U * du_m + 4 * U * abs(self.acc) + 1e-30
         assert np.all(np.abs(host(self.d_down) - self.acc - d_down) <= tol_dd)
@@ -205,7 +205,8 @@ class Case:
 TYPES = [(B, B, B), (B, B, F), (F, F, F), (F, B, F), (B, F, F), (F, B, B), (F, F, B), (B, F, B)]
 SHAPES = [(1, 64, 64, 4, 1, "one"), (1, 33, 7, 1, 3, "random"), (5, 100, 36, 3, 2, "mixed"), (64, 512, 200, 16, 9, "random"),
           (65, 256, 128, 16, 4, "random"), (130, 1030, 517, 12, 3, "runs"), (300, 128, 384, 64, 2, "one"),
-          (200, 64, 64, 8, 70, "random"), (129, 320, 264, 33, 2, "runs"), (600, 72, 40, 8, 3, "none")]
+          (200, 64, 64, 8, 70, "random"), (129, 320, 264, 33, 2, "runs"), (600, 72, 40, 8, 3, "none"), (3100, 200, 136, 16, 2, "runs"),
+          (1100, 130, 1000, 48, 1, "one")]
 
 
 @gpu
@@ -287,7 +288,7 @@ def test_in_place_without_base_without_scale(clean, T, y):
 
 
 @gpu
-@pytest.mark.parametrize("T", [20, 700])
+@pytest.mark.parametrize("T", [20, 2500])
 def test_parts_of_the_gradient_and_accumulation(clean, T):
     c = Case(T, 128, 192, 16, 2, ids="runs")
     dx, dd, du = (t.clone() for t in c.backward())
@@ -352,13 +353,13 @@ def test_plan_groups_every_token_once(clean, T, count, kind):
         assert plan[head] == len(want)
         np.testing.assert_array_equal(plan[at:at + 2 * len(want)].reshape(-1, 2), np.array(want).reshape(-1, 2))
         at += up4(2 * (T // tile + count + 1))
-    want = [(l, start[l] + i) for l in range(count) for i in range(0, max(size[l], 1), 512)]
+    want = [(l, start[l] + i) for l in range(count) for i in range(0, max(size[l], 1), 1024)]
     assert plan[5] == len(want)
     got = plan[at:at + 4 * len(want)].reshape(-1, 4)
     np.testing.assert_array_equal(got[:, :2], np.array(want).reshape(-1, 2))
-    many = np.array([size[l] > 512 for l, _ in want])
+    many = np.array([size[l] > 1024 for l, _ in want])
     np.testing.assert_array_equal(got[many, 2], np.arange(many.sum()))
-    assert np.all(got[~many, 2] == -1) and many.sum() <= 2 * (T // 512)
+    assert np.all(got[~many, 2] == -1) and many.sum() <= 2 * (T // 1024)
 
 
 @gpu
