@@ -50,8 +50,10 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _raw_stream(stream: Optional[torch.cuda.Stream]) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _raw_stream(stream: Optional[torch.cuda.Stream], device: int) -> int:
+    """The CUDA stream handle; the current one without making a Stream object
+    (3 us of a 12 us call)."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _s(stream: Optional[torch.cuda.Stream]):
@@ -465,7 +467,7 @@ def quip_adapter_plan(ids: torch.Tensor, count: int, plan: Optional[torch.Tensor
     nb = _adapter_plan_bytes(T, count)
     if plan is None:
         plan = _scratch(nb, stream)
-    L.check(load().quip_adapter_plan(i, T, count, plan.data_ptr(), plan.numel(), _raw_stream(stream)),
+    L.check(load().quip_adapter_plan(i, T, count, plan.data_ptr(), plan.numel(), _raw_stream(stream, dev)),
             "quip_adapter_plan")
     return plan
 
@@ -501,7 +503,7 @@ def quip_adapter_apply(x: torch.Tensor, ids: torch.Tensor, down: torch.Tensor, u
         px, _dtype(x), _row_stride(x), _here("ids", ids, _I32, (T,), dev), T, n, m, pd, pu, _dtype(down), count, r, ps,
         pb, 0 if base is None else _row_stride(base), py, _dtype(y), _row_stride(y),
         None if h is None else _here("h", h, _F32, (T, r), dev), _adapter_plan_ptr(plan, T, count, dev),
-        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _raw_stream(stream)),
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _raw_stream(stream, dev)),
         "quip_adapter_apply")
 
 
@@ -532,7 +534,7 @@ def quip_adapter_backward(x: torch.Tensor, dy: torch.Tensor, ids: torch.Tensor, 
         None if dx is None else _here("dx", dx, (x.dtype,), (T, n), dev, rows=True), 0 if dx is None else _row_stride(dx),
         None if d_down is None else _here("d_down", d_down, _F32, (count, r, n), dev),
         None if d_up is None else _here("d_up", d_up, _F32, (count, r, m), dev), int(accumulate),
-        _adapter_plan_ptr(plan, T, count, dev), ws.data_ptr(), ws.numel(), _raw_stream(stream)),
+        _adapter_plan_ptr(plan, T, count, dev), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)),
         "quip_adapter_backward")
 
 
@@ -559,7 +561,7 @@ def quip_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], logprob:
         None if entropy is None else _here("entropy", entropy, _F32, (T,), dev),
         None if lse is None else _here("lse", lse, _F32, (T,), dev), k,
         None if k == 0 else _here("top_values", top_values, _F32, (T, k), dev),
-        None if k == 0 else _here("top_ids", top_ids, _I32, (T, k), dev), _raw_stream(stream)), "quip_logprobs")
+        None if k == 0 else _here("top_ids", top_ids, _I32, (T, k), dev), _raw_stream(stream, dev)), "quip_logprobs")
 
 
 def quip_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor], lse: torch.Tensor,
@@ -583,7 +585,7 @@ def quip_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor],
         None if entropy is None else _here("entropy", entropy, _F32, (T,), dev),
         None if g_logprob is None else _here("g_logprob", g_logprob, _F32, (T,), dev),
         None if g_entropy is None else _here("g_entropy", g_entropy, _F32, (T,), dev),
-        d, _row_stride(d_logits), _raw_stream(stream)),
+        d, _row_stride(d_logits), _raw_stream(stream, dev)),
         "quip_logprobs_backward")
 
 

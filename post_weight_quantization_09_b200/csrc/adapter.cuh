@@ -291,26 +291,161 @@ __device__ __forceinline__ bool plan_ok(const PlanView& pv, int T, int count) {
   return ok;
 }
 
-// ---------------------------------------------------------------- vectors
-// A few tokens of one adapter per cluster: NTOK = 1 takes token
-// blockIdx / cluster straight from ids (decode; no plan), NTOK = SMALL the
-// plan's small tiles.  The CTAs of a cluster share n, exchange their partial
-// h through distributed shared memory (summed in rank order by each), and
-// share m.  All sums are fp32 on the CUDA cores; any type, rank and alignment.
+// ---------------------------------------------------------------- single tokens
+// Decode: one cluster per token, straight from ids (no plan), bound by the
+// latency of its chain of loads.  The CTAs of a cluster share n and m.  All
+// that does not wait for h is asked for at once: P and x for the shrink, and
+// each thread's first columns of Q and the base for the expand.  Every CTA
+// stores its partial h into all others' shared memory and, past one cluster
+// barrier, adds them up in rank order.  fp32 on the CUDA cores; any type,
+// rank and alignment.
 constexpr int VT = 256;                        // threads per CTA
-template <int NTOK> __host__ __device__ constexpr int vec_rows() { return NTOK == 1 ? 2 : 4; }   // rows of P per warp task
-template <int NTOK> __host__ __device__ constexpr int vec_cols() { return NTOK == 1 ? 4096 : 1024; }   // of x staged at once
+constexpr int EARLY = 16;                      // rows of Q asked for at once
+constexpr int TOKEN_CTAS = 8;                  // of a cluster, at most
 
-template <int NTOK>
-inline size_t vec_smem(int r) {
-  return sizeof(float) * ((size_t)NTOK * vec_cols<NTOK>() + (size_t)(VT / 32) * NTOK * vec_rows<NTOK>() +
-                          3 * (size_t)NTOK * up4(r) + 16);
+// Four consecutive values as they lie in memory.
+template <typename T> struct Four;
+template <> struct Four<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p, bool vec, int left) { v = load4(p, vec, left); }
+  __device__ __forceinline__ float4 get() const { return v; }
+};
+template <> struct Four<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool vec, int left) {
+    if (vec && left >= 4) {
+      v = __ldg(reinterpret_cast<const uint2*>(p));
+    } else {
+      auto at = [&](int i) { return i < left ? (uint32_t)__bfloat16_as_ushort(p[i]) : 0u; };
+      v = make_uint2(at(0) | at(1) << 16, at(2) | at(3) << 16);
+    }
+  }
+  __device__ __forceinline__ float4 get() const {
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xFFFF0000u));
+  }
+};
+
+template <typename TX, typename TW, typename TY>
+__global__ void __launch_bounds__(VT, sizeof(TW) == 2 ? 4 : 2)
+    k_adapter_token(const __grid_constant__ ApplyArgs<TX, TW, TY> a, const int32_t* __restrict__ ids) {
+  constexpr int R = 2;                         // rows of P per warp at once
+  __shared__ float parts[TOKEN_CTAS][MAX_RANK];    // written by the cluster
+  __shared__ float hs[MAX_RANK];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = a.r;
+  const int64_t token = blockIdx.x / nc;
+  auto running = cluster.barrier_arrive();     // the others' shared memory may be written past this
+  pdl_wait_then_release();
+  int l = ids[token];
+  if (l >= a.count && rank == 0 && tid == 0) record_status(QUIP_ERR_ARG);
+  if (l >= a.count) l = -1;
+  const int m_per = ((a.m + nc - 1) / nc + 3) / 4 * 4, m0 = min(a.m, rank * m_per), m1 = min(a.m, m0 + m_per);
+  const int n_per = ((a.n + nc - 1) / nc + 3) / 4 * 4, n0 = min(a.n, rank * n_per), n1 = min(a.n, n0 + n_per);
+  const TX* x = a.x + token * a.ldx;
+  const TY* base = a.base ? a.base + token * a.ldb : nullptr;
+  TY* y = a.y ? a.y + token * a.ldy : nullptr;
+  const int c0 = m0 + 4 * tid;                 // this thread's first columns
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (l < 0) {                                 // no adapter: y = base, h = 0
+    if (rank == 0 && a.h)
+      for (int i = tid; i < r; i += VT) a.h[token * r + i] = 0.f;
+    if (y && a.y != a.base)
+      for (int c = c0; c < m1; c += 4 * VT) add4(y + c, base ? base + c : nullptr, zero, a.vec_y, m1 - c);
+    cluster.barrier_wait(std::move(running));
+    return;
+  }
+  const TW* P = a.P + (int64_t)l * r * a.n;
+  const TW* Q = a.Q + (int64_t)l * r * a.m;
+  Four<TW> early[EARLY];
+  Four<TY> early_base;
+  if (y && c0 < m1) {
+#pragma unroll
+    for (int j = 0; j < EARLY; ++j) early[j].load(Q + (int64_t)min(j, r - 1) * a.m + c0, a.vec_q, m1 - c0);
+    if (base) early_base.load(base + c0, a.vec_y, m1 - c0);
+  }
+  cluster.barrier_wait(std::move(running));
+  for (int j0 = R * warp; j0 < r; j0 += R * (VT / 32)) {
+    float acc[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) acc[k] = 0.f;
+#pragma unroll 4
+    for (int c = n0 + 4 * lane; c < n1; c += 128) {
+      Four<TX> xv;
+      xv.load(x + c, a.vec_x, n1 - c);
+      const float4 v = xv.get();
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        Four<TW> wv;
+        wv.load(P + (int64_t)min(j0 + k, r - 1) * a.n + c, a.vec_p, n1 - c);
+        const float4 w = wv.get();
+        acc[k] = fmaf(w.x, v.x, acc[k]);
+        acc[k] = fmaf(w.y, v.y, acc[k]);
+        acc[k] = fmaf(w.z, v.z, acc[k]);
+        acc[k] = fmaf(w.w, v.w, acc[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      acc[k] = warp_sum(acc[k]);
+      if (lane < nc && j0 + k < r) *cluster.map_shared_rank(&parts[rank][j0 + k], lane) = acc[k];
+    }
+  }
+  cluster.sync();
+  const float scale = a.scale ? a.scale[l] : 1.f;
+  if (tid < r) {
+    float v = 0.f;
+    for (int c = 0; c < nc; ++c) v += parts[c][tid];
+    hs[tid] = v * scale;
+    if (rank == 0 && a.h) a.h[token * r + tid] = a.h_scaled ? v * scale : v;
+  }
+  __syncthreads();
+  if (!y) return;
+  auto add = [&](float4& acc, const float4& w, float v) {
+    acc.x = fmaf(w.x, v, acc.x);
+    acc.y = fmaf(w.y, v, acc.y);
+    acc.z = fmaf(w.z, v, acc.z);
+    acc.w = fmaf(w.w, v, acc.w);
+  };
+  for (int c = c0; c < m1; c += 4 * VT) {
+    float4 acc = zero;
+    if (c != c0) {
+#pragma unroll
+      for (int j = 0; j < EARLY; ++j) early[j].load(Q + (int64_t)min(j, r - 1) * a.m + c, a.vec_q, m1 - c);
+      if (base) early_base.load(base + c, a.vec_y, m1 - c);
+    }
+#pragma unroll
+    for (int j = 0; j < EARLY; ++j)
+      if (j < r) add(acc, early[j].get(), hs[j]);
+#pragma unroll 8
+    for (int j = EARLY; j < r; ++j) {
+      Four<TW> w;
+      w.load(Q + (int64_t)j * a.m + c, a.vec_q, m1 - c);
+      add(acc, w.get(), hs[j]);
+    }
+    if (base) {
+      const float4 b = early_base.get();
+      acc = make_float4(b.x + acc.x, b.y + acc.y, b.z + acc.z, b.w + acc.w);
+    }
+    add4<TY>(y + c, nullptr, acc, a.vec_y, m1 - c);
+  }
 }
 
-template <int NTOK, typename TX, typename TW, typename TY>
+// ---------------------------------------------------------------- vectors
+// For the types and ranks that the tensor-core tiles do not take: the plan's
+// tiles of up to SMALL tokens of one adapter, one cluster each.  Its CTAs
+// share n, exchange their partial h through distributed shared memory
+// (summed in rank order by each), and share m.  fp32 on the CUDA cores.
+constexpr int NTOK = SMALL, VROWS = 4, VCOLS = 1024;   // tokens; rows of P per warp task; columns of x staged at once
+inline size_t vec_smem(int r) {
+  return sizeof(float) * ((size_t)NTOK * VCOLS + (size_t)(VT / 32) * NTOK * VROWS + 2 * (size_t)NTOK * up4(r));
+}
+
+template <typename TX, typename TW, typename TY>
 __global__ void __launch_bounds__(VT)
-    k_adapter_vec(const __grid_constant__ ApplyArgs<TX, TW, TY> a, const int32_t* __restrict__ ids, void* plan) {
-  constexpr int R = vec_rows<NTOK>(), COLS = vec_cols<NTOK>();
+    k_adapter_vec(const __grid_constant__ ApplyArgs<TX, TW, TY> a, void* plan) {
+  constexpr int R = VROWS, COLS = VCOLS;
   extern __shared__ __align__(16) float sm[];
   __shared__ int tok[NTOK];
   cg::cluster_group cluster = cg::this_cluster();
@@ -318,20 +453,11 @@ __global__ void __launch_bounds__(VT)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int unit = blockIdx.x / nc;
   pdl_wait_then_release();
-  int l, cnt = 1;
-  if constexpr (NTOK == 1) {
-    l = ids[unit];
-    if (l >= a.count && rank == 0 && tid == 0) record_status(QUIP_ERR_ARG);
-    if (l < 0 || l >= a.count) l = a.count;
-    if (tid == 0) tok[0] = unit;
-  } else {
-    const PlanView pv = plan_view(plan, a.T, a.count);
-    if (!plan_ok(pv, a.T, a.count) || unit >= pv.head[H_SMALL]) return;    // the whole cluster
-    const int2 tile = pv.small[unit];
-    l = tile.x;
-    cnt = min(NTOK, pv.start[l + 1] - tile.y);
-    if (tid < NTOK) tok[tid] = tid < cnt ? pv.order[tile.y + tid] : -1;
-  }
+  const PlanView pv = plan_view(plan, a.T, a.count);
+  if (!plan_ok(pv, a.T, a.count) || unit >= pv.head[H_SMALL]) return;      // the whole cluster
+  const int2 tile = pv.small[unit];
+  const int l = tile.x, cnt = min(NTOK, pv.start[l + 1] - tile.y);
+  if (tid < NTOK) tok[tid] = tid < cnt ? pv.order[tile.y + tid] : -1;
   __syncthreads();
   const int r = a.r, r4 = (int)up4(r);
   float* xs = sm;                              // [NTOK][COLS]

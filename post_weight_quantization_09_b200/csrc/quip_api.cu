@@ -1929,19 +1929,29 @@ cudaError_t adapter_plan(const int32_t* ids, int64_t T, int64_t count, void* pla
 // Tokens up to which a cluster per token, without a plan, is taken.
 constexpr int64_t kAdapterDirect = 64;
 
-template <int NTOK, typename TX, typename TW, typename TY>
-cudaError_t adapter_vec(const ad::ApplyArgs<TX, TW, TY>& a, const int32_t* ids, void* plan, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  auto* kernel = ad::k_adapter_vec<NTOK, TX, TW, TY>;
-  cudaError_t e = allow_smem(kernel, (int)ad::vec_smem<NTOK>(ad::MAX_RANK), done);
-  if (e != cudaSuccess) return e;
-  // CTAs per cluster: as the SMs are filled and each still has some columns
-  const int64_t units = NTOK == 1 ? a.T : ad::max_tiles(a.T, a.count, NTOK);
-  const int64_t likely = NTOK == 1 ? a.T : (a.T + NTOK - 1) / NTOK;
+// CTAs per cluster of up to 8: as the SMs are filled and each still has some
+// columns.
+unsigned adapter_cluster(int64_t units, int64_t widest) {
   unsigned nc = 1;
-  while (nc < 8 && likely * nc < 4 * (int64_t)num_sms() && std::max(a.n, a.m) >= 256 * (int64_t)nc) nc *= 2;
+  while (nc < ad::TOKEN_CTAS && units * nc < 4 * (int64_t)num_sms() && widest >= 256 * (int64_t)nc) nc *= 2;
+  return nc;
+}
+template <typename TX, typename TW, typename TY>
+cudaError_t adapter_token(const ad::ApplyArgs<TX, TW, TY>& a, const int32_t* ids, cudaStream_t st) {
+  const unsigned nc = adapter_cluster(a.T, std::max(a.n, a.m));
+  LaunchScope ls("k_adapter_token", st);
+  return launch_cluster(ad::k_adapter_token<TX, TW, TY>, (unsigned)a.T * nc, ad::VT, 0, nc, true, st, a, ids);
+}
+template <typename TX, typename TW, typename TY>
+cudaError_t adapter_vec(const ad::ApplyArgs<TX, TW, TY>& a, void* plan, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  auto* kernel = ad::k_adapter_vec<TX, TW, TY>;
+  cudaError_t e = allow_smem(kernel, (int)ad::vec_smem(ad::MAX_RANK), done);
+  if (e != cudaSuccess) return e;
+  const unsigned nc = adapter_cluster((a.T + ad::NTOK - 1) / ad::NTOK, std::max(a.n, a.m));
   LaunchScope ls("k_adapter_vec", st);
-  return launch_cluster(kernel, (unsigned)(units * nc), ad::VT, ad::vec_smem<NTOK>(a.r), nc, true, st, a, ids, plan);
+  return launch_cluster(kernel, (unsigned)(ad::max_tiles(a.T, a.count, ad::SMALL) * nc), ad::VT, ad::vec_smem(a.r), nc,
+                        true, st, a, plan);
 }
 
 // Whether eight values from each row's start are 16-byte loads.
@@ -2025,7 +2035,7 @@ cudaError_t adapter_apply(ad::ApplyArgs<TX, TW, TY> a, const int32_t* ids, void*
   a.vec_x = rows_of_four(a.x, ldx, sizeof(TX));
   a.vec_p = rows_of_four(a.P, a.n, sizeof(TW));
   a.vec_q = rows_of_four(a.Q, a.m, sizeof(TW));
-  return plan ? adapter_vec<ad::SMALL>(a, ids, plan, st) : adapter_vec<1>(a, ids, nullptr, st);
+  return plan ? adapter_vec(a, plan, st) : adapter_token(a, ids, st);
 }
 
 // P, Q: the factors of the direction (down, up forward; up, down for dx).
