@@ -411,10 +411,11 @@ quip_status quip_qmatvec(const quip_transform* tf, const uint32_t* packed, int64
  *   h     : device T x r fp32, or NULL: kept for quip_adapter_backward.
  *   plan  : from quip_adapter_plan for these ids, T and count (a model makes
  *           it once per batch for all its layers), or NULL: the call makes its
- *           own in ws where it needs one.  A plan of another T or count sets
- *           QUIP_ERR_ARG in the status word and nothing is written.
- *   ws    : quip_adapter_workspace_size(..., 0), or NULL with T <= 64, or with
- *           both a plan and h.
+ *           own in ws where it needs one (small batches use none).  A plan of
+ *           another T or count, where it is used, sets QUIP_ERR_ARG in the
+ *           status word and nothing is written.
+ *   ws    : quip_adapter_workspace_size(..., 0) bytes, none (NULL) where that
+ *           is 0 (small batches) or where both a plan and h are given.
  * Sums are fp32; y is rounded once.  1 <= r <= QUIP_ADAPTER_MAX_RANK,
  * 1 <= count <= QUIP_ADAPTER_MAX_COUNT, T <= 2^22, n, m <= 2^24; T = 0 does
  * nothing.  Any alignment and strides; 16-byte aligned rows of bf16 are

@@ -439,10 +439,6 @@ def _scratch(nbytes: int, stream) -> torch.Tensor:
         return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
 
-# below this many tokens quip_adapter_apply needs neither plan nor workspace
-_ADAPTER_DIRECT = 64
-
-
 @functools.lru_cache(maxsize=256)
 def quip_adapter_workspace_size(T: int, n: int, m: int, r: int, count: int, backward: bool = False) -> int:
     nb = ctypes.c_size_t()
@@ -497,8 +493,10 @@ def quip_adapter_apply(x: torch.Tensor, ids: torch.Tensor, down: torch.Tensor, u
     py = _here("y", y, _FLOATS, (T, m), dev, rows=True)
     count, r, pd, pu, ps = _adapter_factors(down, up, scale, n, m, dev)
     pb = None if base is None else _here("base", base, (y.dtype,), (T, m), dev, rows=True)
-    if ws is None and (plan is None or h is None) and T > _ADAPTER_DIRECT:
-        ws = _scratch(quip_adapter_workspace_size(T, n, m, r, count), stream)
+    if ws is None and (plan is None or h is None):
+        nb = quip_adapter_workspace_size(T, n, m, r, count)
+        if nb:
+            ws = _scratch(nb, stream)
     L.check(load().quip_adapter_apply(
         px, _dtype(x), _row_stride(x), _here("ids", ids, _I32, (T,), dev), T, n, m, pd, pu, _dtype(down), count, r, ps,
         pb, 0 if base is None else _row_stride(base), py, _dtype(y), _row_stride(y),

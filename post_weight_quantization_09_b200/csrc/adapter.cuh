@@ -633,7 +633,7 @@ __host__ __device__ inline int shrink_stage(int r16) { return pieces<TX>() * XT_
 // and a warp to multiply.
 template <bool CP> __host__ __device__ constexpr int stage_warps() { return CP ? 2 : 4; }
 template <bool CP> __host__ __device__ constexpr int stage_threads() { return 32 * (4 * stage_warps<CP>() + 1); }
-__host__ __device__ inline int shrink_stages(int stage) { return stage <= 24 * 1024 ? 4 : 3; }
+__host__ __device__ inline int shrink_stages(int stage) { return stage <= 24 * 1024 || (stage > 32 * 1024 && stage <= 55 * 1024) ? 4 : 3; }
 template <typename TX, typename TW>
 __host__ __device__ inline int shrink_smem(int r16) {
   const int stage = shrink_stage<TX, TW>(r16);
@@ -695,18 +695,21 @@ template <> struct Eight<__nv_bfloat16> {
   }
   __device__ __forceinline__ void store(uint8_t* at, int) const { *reinterpret_cast<uint4*>(at) = v; }
 };
-// Eight fp32 values as three pieces, `step` bytes apart.
+// Eight fp32 values as NP bf16 pieces, `step` bytes apart: each piece rounds
+// what the ones before it leave (as split3, two values at a time).
 template <int NP>
 __device__ __forceinline__ void store_pieces(uint8_t* at, int step, const float (&f)[8]) {
-  uint32_t w[3][4];
+  uint32_t w[NP][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    __nv_bfloat16 a[3], b[3];
-    split3(f[2 * i], a[0], a[1], a[2]);
-    split3(f[2 * i + 1], b[0], b[1], b[2]);
+    float a = f[2 * i], b = f[2 * i + 1];
 #pragma unroll
-    for (int p = 0; p < NP; ++p)
-      w[p][i] = (uint32_t)__bfloat16_as_ushort(a[p]) | (uint32_t)__bfloat16_as_ushort(b[p]) << 16;
+    for (int p = 0; p < NP; ++p) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+      w[p][i] = *reinterpret_cast<const uint32_t*>(&v);
+      a -= __uint_as_float(w[p][i] << 16);
+      b -= __uint_as_float(w[p][i] & 0xFFFF0000u);
+    }
   }
 #pragma unroll
   for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(at + p * step) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
@@ -777,14 +780,19 @@ __global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
       uint8_t* xs = sm + s * stage;
       uint8_t* ps = xs + PX * XT_BYTES;
       auto spot = [&](int row) { return row * 128 + ((ch ^ (row & 7)) << 4); };
+      // the lane's rows of x are those of every block
+      constexpr int ROWS = TILE / (4 * SW), BATCH = 4;
+      int mine[ROWS];
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) mine[k] = tok[row0 + 4 * SW * k];
       for (int i = s; i < steps; i += stages) {
         if (i >= stages) ok = ok && mbar_wait(&empty[s], (uint32_t)((i / stages - 1) & 1));
         const int c = 64 * (k0 + i) + 8 * ch, left = a.n - c;
         if constexpr (CP) {
           const __nv_bfloat16* x = a.x + (c < a.n ? c : 0);
-#pragma unroll 8
-          for (int row = row0; row < cnt; row += 4 * SW)    // rows past the tile's tokens only feed their own sums
-            cp16(xs + spot(row), x + (int64_t)tok[row] * a.ldx, c < a.n);
+#pragma unroll
+          for (int k = 0; k < ROWS; ++k)       // rows past the tile's tokens only feed their own sums
+            if (mine[k] >= 0) cp16(xs + spot(row0 + 4 * SW * k), x + (int64_t)mine[k] * a.ldx, c < a.n);
 #pragma unroll 4
           for (int row = row0; row < r16; row += 4 * SW) {
             const bool there = row < r && c < a.n;
@@ -792,19 +800,36 @@ __global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
           }
           cp_wait_all();
         } else {
-#pragma unroll 4
-          for (int row = row0; row < cnt; row += 4 * SW) {
-            Eight<TX> v;
-            v.zero();
-            if (left > 0) v.load(a.x + (int64_t)tok[row] * a.ldx + c, a.vec_x, left);
-            v.store(xs + spot(row), XT_BYTES);
+          // batches of loads, then their stores: a load does not pass a store by itself
+          Eight<TW> w[BATCH];
+          auto load_p = [&](int row) {
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+              const int j = row + 4 * SW * k;
+              w[k].zero();
+              if (j < r && left > 0) w[k].load(P + (int64_t)j * a.n + c, a.vec_p, left);
+            }
+          };
+          load_p(row0);
+#pragma unroll
+          for (int k0 = 0; k0 < ROWS; k0 += BATCH) {
+            Eight<TX> v[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+              v[k].zero();
+              if (mine[k0 + k] >= 0 && left > 0) v[k].load(a.x + (int64_t)mine[k0 + k] * a.ldx + c, a.vec_x, left);
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k)
+              if (mine[k0 + k] >= 0) v[k].store(xs + spot(row0 + 4 * SW * (k0 + k)), XT_BYTES);
           }
-#pragma unroll 4
-          for (int row = row0; row < r16; row += 4 * SW) {
-            Eight<TW> v;
-            v.zero();
-            if (row < r && left > 0) v.load(P + (int64_t)row * a.n + c, a.vec_p, left);
-            v.store(ps + spot(row), r16 * 128);
+          for (int row = row0; row < r16; row += 4 * SW * BATCH) {
+            if (row > row0) load_p(row);
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+              const int j = row + 4 * SW * k;
+              if (j < r16) w[k].store(ps + spot(j), r16 * 128);
+            }
           }
         }
         fence_proxy_async_smem();
@@ -997,13 +1022,26 @@ __global__ void __launch_bounds__(ET, 1)
                        : "memory");
       } else if (i < steps && a.base && busy) {
         const int c = (b0 + i) * CB + col, left = a.m - c;
-#pragma unroll 2
-        for (int v = 0; v < 16; ++v) {
-          const int tr = 2 * v + lane / 16, t = tok[token0 + tr];
-          if (t < 0) continue;
-          const TY* from = a.base + (int64_t)t * a.ldb + c;
-          if (a.vec_y && left >= EV) cp16(rows + piece(tr, lane % 16), from, true);
-          else *reinterpret_cast<uint4*>(rows + piece(tr, lane % 16)) = load_vec(from, false, left);
+        if (a.vec_y && (b0 + i + 1) * CB <= a.m) {
+#pragma unroll 4
+          for (int v = 0; v < 16; ++v) {
+            const int tr = 2 * v + lane / 16;
+            const int64_t t = tok[token0 + tr];
+            if (t >= 0) cp16(rows + piece(tr, lane % 16), a.base + t * a.ldb + c, true);
+          }
+          return;
+        }
+        for (int v0 = 0; v0 < 16; v0 += 4) {   // four loads, then their stores
+          uint4 u[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int64_t t = tok[token0 + 2 * (v0 + v) + lane / 16];
+            u[v] = make_uint4(0u, 0u, 0u, 0u);
+            if (t >= 0) u[v] = load_vec(a.base + t * a.ldb + c, a.vec_y, left);
+          }
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            *reinterpret_cast<uint4*>(rows + piece(2 * (v0 + v) + lane / 16, lane % 16)) = u[v];
         }
       }
     };
@@ -1023,12 +1061,20 @@ __global__ void __launch_bounds__(ET, 1)
         }
         cp_wait_all();
       } else {
-#pragma unroll 4
-        for (int j = lane / CH; j < r16; j += 32 / CH) {
-          Eight<TW> v;
-          v.zero();
-          if (j < r && c < a.m) v.load(Q + (int64_t)j * a.m + c, a.vec_q, a.m - c);
-          v.store(to + spot(j), r16 * 2 * (CB > 64 ? CB : 64));
+        constexpr int BATCH = 4;
+        for (int j0 = lane / CH; j0 < r16; j0 += 32 / CH * BATCH) {
+          Eight<TW> v[BATCH];
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const int j = j0 + 32 / CH * k;
+            v[k].zero();
+            if (j < r && c < a.m) v[k].load(Q + (int64_t)j * a.m + c, a.vec_q, a.m - c);
+          }
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const int j = j0 + 32 / CH * k;
+            if (j < r16) v[k].store(to + spot(j), r16 * 2 * (CB > 64 ? CB : 64));
+          }
         }
       }
       fence_proxy_async_smem();
@@ -1160,7 +1206,7 @@ __global__ void __launch_bounds__(ET, 1)
             to[offset[v]] = *reinterpret_cast<const uint4*>(rows + piece(2 * v + lane / 16, lane % 16));
         } else if (busy && ok) {
           const int c = (b0 + i) * CB + col, left = a.m - c;
-#pragma unroll 2
+#pragma unroll 4
           for (int v = 0; v < 16; ++v) {
             const int tr = 2 * v + lane / 16, t = tok[token0 + tr];
             if (t >= 0)
@@ -1397,13 +1443,18 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
             }
             cp_wait_all();
           } else {
-#pragma unroll 4
-            for (int k = 0; k < ROWS; k += AT_ONCE) {
-              const int row = k + lane / CHS, t = __shfl_sync(0xffffffffu, mine, row);
-              Eight<TX> v;
-              v.zero();
-              if (t >= 0 && left > 0) v.load(a.x + (int64_t)t * a.ldx + c, a.vec_x, left);
-              v.store(xs + spot(row0 + row), H * XB);
+            constexpr int BATCH = ROWS / AT_ONCE < 4 ? ROWS / AT_ONCE : 4;
+#pragma unroll
+            for (int k0 = 0; k0 < ROWS; k0 += AT_ONCE * BATCH) {
+              Eight<TX> v[BATCH];
+#pragma unroll
+              for (int k = 0; k < BATCH; ++k) {
+                const int t = __shfl_sync(0xffffffffu, mine, k0 + AT_ONCE * k + lane / CHS);
+                v[k].zero();
+                if (t >= 0 && left > 0) v[k].load(a.x + (int64_t)t * a.ldx + c, a.vec_x, left);
+              }
+#pragma unroll
+              for (int k = 0; k < BATCH; ++k) v[k].store(xs + spot(row0 + k0 + AT_ONCE * k + lane / CHS), H * XB);
             }
           }
           fence_proxy_async_smem();

@@ -1926,8 +1926,11 @@ cudaError_t adapter_plan(const int32_t* ids, int64_t T, int64_t count, void* pla
                     (int)count, plan);
 }
 
-// Tokens up to which a cluster per token, without a plan, is taken.
-constexpr int64_t kAdapterDirect = 64;
+// Whether a cluster per token, without a plan, is taken: it reads a token's
+// adapter from L2 for every token, the tiles pay for the plan and their start.
+// 4096 -> 11008, rank 16, 32 adapters: 27 and 57 us for 128 tokens, 47 and 71
+// for 256, 84 and 75 for 512; rank 64: 149 and 69 us for 128.
+bool adapter_direct(int64_t T, int64_t r) { return T <= 16 || T * r <= 4096; }
 
 // CTAs per cluster of up to 8: as the SMs are filled and each still has some
 // columns.
@@ -1965,13 +1968,15 @@ cudaError_t adapter_shrink(const ad::ApplyArgs<TX, TW, float>& a, void* plan, cu
   auto* kernel = ad::k_adapter_shrink<TX, TW, CP>;
   cudaError_t e = allow_smem(kernel, 226 * 1024, done);
   if (e != cudaSuccess) return e;
-  // CTAs per cluster: as many as two per SM hold at once with a part-filled
-  // tile per adapter, each with a block at least
+  // CTAs per cluster: as many as the SMs hold at once (one or two each) with a
+  // part-filled tile per adapter, each with a block at least
+  const int smem = ad::shrink_smem<TX, TW>((a.r + 15) / 16 * 16);
+  const int64_t resident = (CP && smem <= 112 * 1024 ? 2 : 1) * (int64_t)num_sms();
   const int64_t likely = (a.T + ad::TILE - 1) / ad::TILE + std::min<int64_t>(a.count, a.T / 16), blocks = (a.n + 63) / 64;
-  const unsigned nc = (unsigned)std::min<int64_t>(std::min<int64_t>(8, blocks), std::max<int64_t>(1, 2 * num_sms() / likely));
+  const unsigned nc = (unsigned)std::min<int64_t>(std::min<int64_t>(8, blocks), std::max<int64_t>(1, resident / likely));
   LaunchScope ls("k_adapter_shrink", st);
   return launch_cluster(kernel, (unsigned)(ad::max_tiles(a.T, a.count, ad::TILE) * nc), ad::stage_threads<CP>(),
-                        ad::shrink_smem<TX, TW>((a.r + 15) / 16 * 16), nc, true, st, a, plan);
+                        smem, nc, true, st, a, plan);
 }
 
 template <bool CP, typename TW, typename TY>
@@ -2185,7 +2190,7 @@ quip_status quip_adapter_workspace_size(int64_t T, int64_t n, int64_t m, int64_t
   *bytes = 0;
   quip_status s = adapter_shape(T, n, m, r, count);
   if (s != QUIP_OK) return s;
-  *bytes = adapter_ws(T, n, m, r, count, backward != 0).total;
+  *bytes = !backward && adapter_direct(T, r) ? 0 : adapter_ws(T, n, m, r, count, backward != 0).total;
   return QUIP_OK;
 }
 
@@ -2204,7 +2209,7 @@ quip_status quip_adapter_apply(const void* x, int x_dtype, int64_t ldx, const in
   if (regions_overlap(x, ldx, n, type_bytes(x_dtype), y, ldy, m, ys, T)) return QUIP_ERR_ARG;
   cudaStream_t st = S(stream);
   void* pl = nullptr;
-  if (T > kAdapterDirect) {
+  if (!adapter_direct(T, r)) {
     const AdapterWs w = adapter_ws(T, n, m, r, count, false);
     pl = const_cast<void*>(plan);
     if (!pl || !h) {
@@ -2256,7 +2261,7 @@ quip_status quip_adapter_backward(const void* x, int x_dtype, int64_t ldx, const
   if (T > 0 && (dx || d_down)) {
     const AdapterCall c{dy, lddy, up, dx ? down : up, scale, dx ? dx_base : nullptr, lddb, dx, lddx, dh,
                         T, m, n, r, count, true};
-    QCHECK(adapter_dispatch(dy_dtype, w_dtype, x_dtype, c, ids, T <= kAdapterDirect ? nullptr : pl, st));
+    QCHECK(adapter_dispatch(dy_dtype, w_dtype, x_dtype, c, ids, adapter_direct(T, r) ? nullptr : pl, st));
   }
   if (d_down || d_up) {
     uint8_t* pieces = reinterpret_cast<uint8_t*>(w8 + w.pieces);

@@ -81,7 +81,7 @@ def test_refusals_answer_on_the_host():
     assert fw(base=p(6), ldy=40) == L.QUIP_ERR_ARG                   # the same buffer, other rows
     assert fw(base=ctypes.c_void_p(p(6).value + 4)) == L.QUIP_ERR_ARG
     assert fw(y=p(0), base=None) == L.QUIP_ERR_ARG                   # y over x
-    assert fw(ws=None) == fw(wsb=16) == fw(ws=ctypes.c_void_p(0x1004)) == L.QUIP_ERR_WORKSPACE
+    assert fw(T=1100, ws=None) == fw(T=1100, wsb=16) == fw(T=1100, ws=ctypes.c_void_p(0x1004)) == L.QUIP_ERR_WORKSPACE
     assert fw(T=0, x=None) == L.QUIP_OK
 
     def bw(x=p(0), xt=0, ldx=64, dy=p(1), dyt=0, lddy=32, ids=p(2), T=100, n=64, m=32, down=p(3), up=p(4), r=4, h=p(5),
@@ -204,8 +204,8 @@ class Case:
 
 TYPES = [(B, B, B), (B, B, F), (F, F, F), (F, B, F), (B, F, F), (F, B, B), (F, F, B), (B, F, B)]
 SHAPES = [(1, 64, 64, 4, 1, "one"), (1, 33, 7, 1, 3, "random"), (5, 100, 36, 3, 2, "mixed"), (64, 512, 200, 16, 9, "random"),
-          (65, 256, 128, 16, 4, "random"), (130, 1030, 517, 12, 3, "runs"), (300, 128, 384, 64, 2, "one"),
-          (200, 64, 64, 8, 70, "random"), (129, 320, 264, 33, 2, "runs"), (600, 72, 40, 8, 3, "none"), (3100, 200, 136, 16, 2, "runs"),
+          (300, 256, 128, 16, 4, "random"), (400, 1030, 517, 12, 3, "runs"), (300, 128, 384, 64, 2, "one"),
+          (560, 64, 64, 8, 70, "random"), (130, 96, 72, 12, 5, "runs"), (129, 320, 264, 33, 2, "runs"), (600, 72, 40, 8, 3, "none"), (3100, 200, 136, 16, 2, "runs"),
           (1100, 130, 1000, 48, 1, "one")]
 
 
@@ -243,7 +243,7 @@ def test_large_ranks_and_widths(clean, T, n, m, r, count, ids, x, w, y):
 @gpu
 @pytest.mark.parametrize("x,y", [(B, B), (B, F), (F, F)])
 @pytest.mark.parametrize("pad", [1, 2, 8])
-@pytest.mark.parametrize("T", [3, 140])
+@pytest.mark.parametrize("T", [3, 270])
 def test_strided_rows(clean, T, pad, x, y):
     c = Case(T, 264, 136, 16, 3, x, B, y, "random", pad=pad)
     c.apply()
@@ -255,7 +255,7 @@ def test_strided_rows(clean, T, pad, x, y):
 @gpu
 def test_unaligned_tensors(clean):
     # every operand one element off its 16-byte boundary
-    for T in (4, 150):
+    for T in (4, 300):
         c = Case(T, 256, 128, 16, 2)
         off = lambda t: torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape).copy_(t)
         c.x, c.base, c.dy, c.dx_base, c.down, c.up = (off(t.contiguous()) for t in (c.x, c.base, c.dy, c.dx_base, c.down, c.up))
@@ -267,7 +267,7 @@ def test_unaligned_tensors(clean):
 
 
 @gpu
-@pytest.mark.parametrize("T", [7, 200])
+@pytest.mark.parametrize("T", [7, 600])
 @pytest.mark.parametrize("y", [B, F])
 def test_in_place_without_base_without_scale(clean, T, y):
     c = Case(T, 128, 256, 8, 3, y=y)
@@ -367,13 +367,13 @@ def test_bad_ids_and_plans_are_reported():
     Q.load()
     Q.quip_sync_status()
     for T in (3, 200):
-        c = Case(T, 64, 64, 4, 2)
+        c = Case(T, 64, 64, 32, 2)
         c.ids[1] = 2
         c.apply()
         assert Q.quip_sync_status() == L.QUIP_ERR_ARG
         c.ids[1] = -1
         c.check_apply()
-    c = Case(200, 64, 64, 4, 2)
+    c = Case(200, 64, 64, 32, 2)
     plan = Q.quip_adapter_plan(c.ids, 2)
     plan.view(torch.int32)[1] = 199                      # a plan of another batch
     c.y.fill_(7)
