@@ -838,27 +838,28 @@ __global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
       }
     }
   } else if (lane == 0) {
+    // descriptors' addresses count 16 bytes: stages and steps are added to them
     const uint32_t idesc = make_idesc_bf16(TILE, r16, 0, 0);
+    const uint64_t x0 = make_sw128_desc(smem_u32(sm), 16, 1024), p0 = x0 + (uint64_t)(PX * XT_BYTES >> 4);
+    const int pp = r16 * 128 >> 4;
+    const uint32_t low = tmem + (uint32_t)((accs - 1) * r16);
     for (int i = 0; i < steps && ok; ++i) {
       const int s = i % stages;
       ok = mbar_wait(&full[s], (uint32_t)((i / stages) & 1));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t xa = smem_u32(sm + s * stage), pa = xa + PX * XT_BYTES;
-      bool small = i > 0;                      // the small terms' accumulator holds something
+      const uint64_t xd = x0 + (uint64_t)(s * stage >> 4), pd = p0 + (uint64_t)(s * stage >> 4);
+      const uint32_t large = tmem + (uint32_t)(i % mains * r16);
 #pragma unroll
       for (int px = 0; px < PX; ++px)
 #pragma unroll
-        for (int pw = 0; pw < PW && px + pw <= 2; ++pw) {
-          const bool main = px + pw == 0;
-          const uint32_t d = tmem + (uint32_t)((main ? i % mains : accs - 1) * r16);
+        for (int pw = 0; pw < PW && px + pw <= 2; ++pw)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f16(d, make_sw128_desc(xa + px * XT_BYTES + kk * 32, 16, 1024),
-                       make_sw128_desc(pa + pw * r16 * 128 + kk * 32, 16, 1024), idesc,
-                       (main ? i >= mains : small) || kk > 0);
-          if (!main) small = true;
-        }
+          for (int kk = 0; kk < 4; ++kk) {
+            const bool main = px + pw == 0, first = (PW > 1 ? px == 0 && pw == 1 : px == 1) && kk == 0;   // of the small terms
+            tc_mma_f16(main ? large : low, xd + (uint64_t)((px * XT_BYTES >> 4) + kk * 2),
+                       pd + (uint64_t)(pw * pp + kk * 2), idesc, main ? (i >= mains || kk > 0) : (i > 0 || !first));
+          }
       tc_commit(&empty[s]);
     }
     if (steps > 0 && ok) tc_commit(&all_done);
@@ -1360,8 +1361,10 @@ struct OuterPair {             // column blocks [0, split) are the first's, the 
   const uint8_t* u[2];
   int split;
 };
-// Resident CTAs, each an equal run of the (column block, chunk) pairs, the
-// chunks inside, so that long and short ones mix.  Warps: the stages', one to
+// Resident CTAs take the (chunk, column block) pairs in turn: those that run at
+// a time read neighbouring columns of the same rows (each CTA a run of chunks
+// of one block took every row's piece from another DRAM page: 2.6 TB/s), and
+// all get long and short chunks alike.  Warps: the stages', one to
 // multiply, others that write a pair's sums while the next is multiplied into
 // the other half of TMEM (where two sets of accumulators fit); each goes
 // through the pairs by itself.
@@ -1383,8 +1386,7 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
   if (!plan_ok(pv, T, count)) return;
   const int chunks = pv.head[H_CHUNKS];
   const int64_t work = (int64_t)chunks * blocks;
-  const int64_t w0 = work * blockIdx.x / gridDim.x, w1 = work * (blockIdx.x + 1) / gridDim.x;
-  if (w0 == w1) return;
+  if (blockIdx.x >= work) return;
   const int r16 = (r + 15) / 16 * 16, accs = tc_accs(r16), mains = accs - 1;
   const int sets = 2 * H * accs * r16 <= TCOLS ? 2 : 1;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1402,18 +1404,18 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
   bool ok = true;
   // pair w's chunk and its number of tokens, looked up one pair ahead
   auto look = [&](int64_t w, int4& chunk, int& cnt) {
-    if (w < w1) {
-      chunk = pv.chunks[w % chunks];
+    if (w < work) {
+      chunk = pv.chunks[w / blocks];
       cnt = max(0, min(CHUNK, pv.start[chunk.x + 1] - chunk.y));
     }
   };
   int4 chunk, next;
   int cnt, next_cnt;
-  look(w0, chunk, cnt);
+  look(blockIdx.x, chunk, cnt);
   int fills = 0, items = 0;                    // stages filled and pairs with tokens before this one
-  for (int64_t w = w0; w < w1; ++w, chunk = next, cnt = next_cnt) {
-    look(w + 1, next, next_cnt);
-    const int l = chunk.x, steps = (cnt + SUB - 1) / SUB, block = (int)(w / chunks), which = block >= both.split;
+  for (int64_t w = blockIdx.x; w < work; w += gridDim.x, chunk = next, cnt = next_cnt) {
+    look(w + gridDim.x, next, next_cnt);
+    const int l = chunk.x, steps = (cnt + SUB - 1) / SUB, block = (int)(w % blocks), which = block >= both.split;
     const OuterArgs<TX>& a = both.a[which];
     const int c0 = (block - (which ? both.split : 0)) * 128 * H;
     if (warp < MW) {
@@ -1464,31 +1466,35 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
       }
     } else if (warp == MW) {
       if (lane == 0) {
+        // The descriptors' addresses count 16 bytes: built once, stages and
+        // steps are added (built for each of 24 products a stage they took
+        // 2 us of this one thread).
         const uint32_t idesc = make_idesc_bf16(128, r16, 1, 0);
+        const uint64_t x0 = make_sw128_desc(smem_u32(sm), 8192, 1024);
+        const uint64_t u0 = make_sw128_desc(smem_u32(sm) + PX * H * XB, 16, 1024);
+        const int up = r16 * 128 >> 4;
         for (int i = 0; i < steps && ok; ++i) {
           const int f = fills + i, s = f % stages, n = items;
           if (i == 0 && n >= sets) ok = mbar_wait(&drained[n % sets], (uint32_t)((n / sets - 1) & 1));
           ok = ok && mbar_wait(&full[s], (uint32_t)((f / stages) & 1));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t xa = smem_u32(sm + s * stage), ua = xa + PX * H * XB;
+          const uint64_t xd = x0 + (uint64_t)(s * stage >> 4), ud = u0 + (uint64_t)(s * stage >> 4);
           const uint32_t set = tmem + (uint32_t)(n % sets * (TCOLS / 2));
 #pragma unroll
           for (int hh = 0; hh < H; ++hh) {
-            bool small = i > 0;
+            const uint32_t large = set + (uint32_t)((hh * accs + i % mains) * r16), low = set + (uint32_t)((hh * accs + accs - 1) * r16);
 #pragma unroll
             for (int px = 0; px < PX; ++px)
 #pragma unroll
-              for (int pu = 0; pu < 3 - px; ++pu) {
-                const bool main = px + pu == 0;
-                const uint32_t d = set + (uint32_t)((hh * accs + (main ? i % mains : accs - 1)) * r16);
+              for (int pu = 0; pu < 3 - px; ++pu)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  tc_mma_f16(d, make_sw128_desc(xa + (px * H + hh) * XB + kk * 2048, 8192, 1024),
-                             make_sw128_desc(ua + pu * r16 * 128 + kk * 32, 16, 1024), idesc,
-                             (main ? i >= mains : small) || kk > 0);
-                if (!main) small = true;
-              }
+                for (int kk = 0; kk < 4; ++kk) {
+                  const bool main = px + pu == 0, first = px + pu == 1 && px == 0 && kk == 0;   // of the small terms
+                  tc_mma_f16(main ? large : low, xd + (uint64_t)(((px * H + hh) * XB + kk * 2048) >> 4),
+                             ud + (uint64_t)(pu * up + kk * 2), idesc,
+                             main ? (i >= mains || kk > 0) : (i > 0 || !first));
+                }
           }
           tc_commit(&empty[s]);
           if (i == steps - 1) tc_commit(&ready[n % sets]);
