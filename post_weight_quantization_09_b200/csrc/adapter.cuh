@@ -1307,9 +1307,10 @@ __global__ void __launch_bounds__(OT) k_adapter_outer(const __grid_constant__ Ou
 // The same on the tensor cores: D[column][j] = x^T u (M = 128 columns, N = r,
 // K = tokens, x MN-major as its rows lie in memory), SUB tokens at a time, two
 // times 128 columns (one with fp32 rows) that share u's tile.  u is cut into
-// three bf16 pieces; the large terms are dealt out over all accumulators but
-// one, which takes the small ones, so few steps meet in each (tc_accs).  The
-// pieces are made once, K-major and swizzled as the tensor core reads them
+// three bf16 pieces that lie one after the other, so one product takes several
+// as more columns of D: its time is that of reading x from shared memory, 60
+// cycles whatever N.  (OuterBlocks: which pieces go together.)  The pieces are
+// made once, K-major and swizzled as the tensor core reads them
 // (k_adapter_pieces), so that a stage takes them by one bulk copy.
 __host__ __device__ inline int64_t max_subs(int64_t T, int64_t count) { return T / SUB + (count < T ? count : T) + 1; }
 __host__ __device__ inline int u_bytes(int r16) { return 3 * r16 * 128; }    // of SUB tokens
@@ -1355,6 +1356,23 @@ __host__ __device__ inline int outer_stages(int stage) {
   const int s = 216 * 1024 / stage;
   return s > 4 ? 4 : s;
 }
+// Accumulators of a half, in blocks of r16 columns whose sum is the result:
+// MAINS sets of `width` blocks that take x's first piece times u's first
+// `width` pieces, a step in turn (few steps meet in each), then `low` blocks
+// for the other terms.  Up to rank 32 all of u in one product; up to 64 u's
+// second and third piece in one; beyond, each by itself.
+struct OuterBlocks {
+  int width, low, total;
+};
+constexpr int MAINS = 2;
+__host__ __device__ inline OuterBlocks outer_blocks(int r16, int px) {
+  OuterBlocks b;
+  b.width = r16 <= 32 ? 3 : 1;
+  b.low = r16 <= 32 ? (px > 1 ? 2 : 0) : r16 <= 64 ? 2 : 1;
+  const int mains = r16 <= 64 ? MAINS : 1;
+  b.total = mains * b.width + b.low;
+  return b;
+}
 template <typename TX>
 struct OuterPair {             // column blocks [0, split) are the first's, the rest the second's
   OuterArgs<TX> a[2];
@@ -1375,7 +1393,7 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
     k_adapter_outer_tc(const __grid_constant__ OuterPair<TX> both, int blocks, void* plan) {
   constexpr int PX = pieces<TX>(), XB = SUB * 256;       // bytes of one piece of SUB tokens x 128 columns
   constexpr int SW = stage_warps<CP>(), MW = 4 * SW, H = outer_halves<TX>();
-  constexpr int CHS = 16 * H, ROWS = SUB / SW, AT_ONCE = 32 / CHS, TCOLS = TC_COLS * H;   // 16-byte columns; a warp's rows
+  constexpr int CHS = 16 * H, ROWS = SUB / SW, AT_ONCE = 32 / CHS, TCOLS = 512;   // 16-byte columns; a warp's rows
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[4], empty[4], ready[2], drained[2];
   __shared__ uint32_t tmem_base;
@@ -1387,8 +1405,9 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
   const int chunks = pv.head[H_CHUNKS];
   const int64_t work = (int64_t)chunks * blocks;
   if (blockIdx.x >= work) return;
-  const int r16 = (r + 15) / 16 * 16, accs = tc_accs(r16), mains = accs - 1;
-  const int sets = 2 * H * accs * r16 <= TCOLS ? 2 : 1;
+  const int r16 = (r + 15) / 16 * 16;
+  const OuterBlocks blk = outer_blocks(r16, PX);
+  const int mains = (blk.total - blk.low) / blk.width, sets = 2 * H * blk.total * r16 <= TCOLS ? 2 : 1;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int stage = outer_stage<TX>(r16), stages = outer_stages(stage);
   if (tid == 0) {
@@ -1469,7 +1488,6 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
         // The descriptors' addresses count 16 bytes: built once, stages and
         // steps are added (built for each of 24 products a stage they took
         // 2 us of this one thread).
-        const uint32_t idesc = make_idesc_bf16(128, r16, 1, 0);
         const uint64_t x0 = make_sw128_desc(smem_u32(sm), 8192, 1024);
         const uint64_t u0 = make_sw128_desc(smem_u32(sm) + PX * H * XB, 16, 1024);
         const int up = r16 * 128 >> 4;
@@ -1479,22 +1497,40 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
           ok = ok && mbar_wait(&full[s], (uint32_t)((f / stages) & 1));
           if (!ok) break;
           tc_fence_after();
-          const uint64_t xd = x0 + (uint64_t)(s * stage >> 4), ud = u0 + (uint64_t)(s * stage >> 4);
+          uint64_t xd = x0 + (uint64_t)(s * stage >> 4);
+          const uint64_t ud = u0 + (uint64_t)(s * stage >> 4);
           const uint32_t set = tmem + (uint32_t)(n % sets * (TCOLS / 2));
+          // x's piece px times `n` pieces of u from pu on, into D's blocks from `to` on
+          auto product = [&](int px, int pu, int n, uint32_t to, bool add) {
+            const uint32_t idesc = make_idesc_bf16(128, n * r16, 1, 0);
 #pragma unroll
-          for (int hh = 0; hh < H; ++hh) {
-            const uint32_t large = set + (uint32_t)((hh * accs + i % mains) * r16), low = set + (uint32_t)((hh * accs + accs - 1) * r16);
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f16(to, xd + (uint64_t)((px * H * XB + kk * 2048) >> 4), ud + (uint64_t)(pu * up + kk * 2), idesc,
+                         add || kk > 0);
+          };
 #pragma unroll
-            for (int px = 0; px < PX; ++px)
-#pragma unroll
-              for (int pu = 0; pu < 3 - px; ++pu)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                  const bool main = px + pu == 0, first = px + pu == 1 && px == 0 && kk == 0;   // of the small terms
-                  tc_mma_f16(main ? large : low, xd + (uint64_t)(((px * H + hh) * XB + kk * 2048) >> 4),
-                             ud + (uint64_t)(pu * up + kk * 2), idesc,
-                             main ? (i >= mains || kk > 0) : (i > 0 || !first));
-                }
+          for (int hh = 0; hh < H; ++hh, xd += XB >> 4) {
+            const uint32_t half = set + (uint32_t)(hh * blk.total * r16), low = half + (uint32_t)(mains * blk.width * r16);
+            product(0, 0, blk.width, half + (uint32_t)(i % mains * blk.width * r16), i >= mains);
+            bool add = i > 0;
+            if (blk.width == 1) {
+              if (blk.low == 2) {
+                product(0, 1, 2, low, add);
+              } else {
+                product(0, 1, 1, low, add);
+                product(0, 2, 1, low, true);
+              }
+              add = true;
+            }
+            if constexpr (PX > 1) {
+              if (blk.low == 2) {
+                product(1, 0, 2, low, add);
+              } else {
+                product(1, 0, 1, low, add);
+                product(1, 1, 1, low, true);
+              }
+              product(2, 0, 1, low, true);
+            }
           }
           tc_commit(&empty[s]);
           if (i == steps - 1) tc_commit(&ready[n % sets]);
@@ -1509,13 +1545,13 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
       const float k = a.scale ? a.scale[l] : 1.f;
       float* out = chunk.z < 0 ? a.out + (int64_t)l * r * a.width : a.partial + (int64_t)chunk.z * r * a.width;
       const bool add = chunk.z < 0 && a.accumulate;
-      const uint32_t at = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + (uint32_t)(n % sets * (TCOLS / 2) + half * accs * r16);
+      const uint32_t at = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + (uint32_t)(n % sets * (TCOLS / 2) + half * blk.total * r16);
       for (int j = 0; j < r16; j += 16) {
         float v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = 0.f;
-        for (int q = accs - 1; q >= 0; --q) {            // the small terms first
-          if (q == accs - 1 ? steps > 0 : q < steps) {
+        for (int q = blk.total - 1; q >= 0; --q) {       // from the small terms on
+          if (q >= mains * blk.width ? steps > 0 : q / blk.width < steps) {
             float t[16];
             tmem_ld16(at + q * r16 + j, t);
 #pragma unroll
