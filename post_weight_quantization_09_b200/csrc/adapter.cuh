@@ -599,8 +599,8 @@ __global__ void __launch_bounds__(VT)
 // memory.
 //
 // Expand: resident CTAs, each an equal run of the (tile, column block) pairs:
-// D[token][column] = h Q (M = 128 tokens, N = the block's columns, K = r, Q MN-major as it lies in
-// memory).  Three warps fetch Q's tiles, one multiplies; the others, in up to
+// D[token][column] = h Q (M = 128 tokens, N = the block's columns, K = r, Q
+// MN-major as it lies in memory).  Three warps fetch Q's tiles, one multiplies; the others, in up to
 // four groups of four, take a block in turn, 32 tokens (TMEM lanes) each: a warp
 // brings its rows of the base to shared memory, 256 bytes at a time by 16
 // neighbouring lanes, adds a row's products there, and sends the sums out as
@@ -617,11 +617,7 @@ __global__ void __launch_bounds__(VT)
 // Loads are gathered by token into shared memory with the 128-byte swizzle,
 // by cp.async where bf16 rows allow 16-byte copies (CP), else through
 // registers, which also cuts fp32 values into pieces and takes any alignment.
-// Each stage has warps of its own that fill it, wait for it and hand it on: the fence between a thread's writes and the tensor core's reads waits
-// for every load that the thread has in flight, so a thread with later stages
-// under way would wait for them at each step (2.9 us a block in the expand
-// step, whatever the rank).
-constexpr int TT = 256;                        // threads per CTA
+// Each stage has warps of its own that fill it, wait for it and hand it on.
 constexpr int TC_COLS = 256;                   // TMEM columns: two CTAs fit an SM (see shrink_smem)
 template <typename T> __host__ __device__ constexpr int pieces() { return sizeof(T) == 2 ? 1 : 3; }
 template <typename TY> __host__ __device__ constexpr int h_pieces() { return sizeof(TY) == 2 ? 2 : 3; }
@@ -633,7 +629,11 @@ __host__ __device__ inline int shrink_stage(int r16) { return pieces<TX>() * XT_
 // and a warp to multiply.
 template <bool CP> __host__ __device__ constexpr int stage_warps() { return CP ? 2 : 4; }
 template <bool CP> __host__ __device__ constexpr int stage_threads() { return 32 * (4 * stage_warps<CP>() + 1); }
-__host__ __device__ inline int shrink_stages(int stage) { return stage <= 24 * 1024 || (stage > 32 * 1024 && stage <= 55 * 1024) ? 4 : 3; }
+// four, but three where that lets two CTAs on an SM (bf16, ranks above 64) or
+// one at all
+__host__ __device__ inline int shrink_stages(int stage) {
+  return stage <= 24 * 1024 || (stage > 32 * 1024 && stage <= 55 * 1024) ? 4 : 3;
+}
 template <typename TX, typename TW>
 __host__ __device__ inline int shrink_smem(int r16) {
   const int stage = shrink_stage<TX, TW>(r16);
@@ -655,12 +655,11 @@ struct ExpandRings {
   int q, rows, smem;
 };
 template <typename TW, typename TY>
-__host__ __device__ inline int expand_tile(int r16) { return pieces<TW>() * r16 * 2 * (expand_cols<TY>() > 64 ? expand_cols<TY>() : 64); }
+__host__ __device__ inline int expand_tile(int r16) { return pieces<TW>() * r16 * 2 * expand_cols<TY>(); }
 template <typename TW, typename TY>
 inline ExpandRings expand_rings(int r16) {
   const int h = h_pieces<TY>() * ((r16 + 63) / 64) * XT_BYTES + 1024, tile = expand_tile<TW, TY>(r16);
   ExpandRings e{QW, 4, 0};
-  while (e.q > 3 && h + e.q * tile + e.rows * ROW_BYTES > EXPAND_MAX) --e.q;
   while (e.rows > 3 && h + e.q * tile + e.rows * ROW_BYTES > EXPAND_MAX) --e.rows;
   while (e.q > 2 && h + e.q * tile + e.rows * ROW_BYTES > EXPAND_MAX) --e.q;
   while (e.rows > 1 && h + e.q * tile + e.rows * ROW_BYTES > EXPAND_MAX) --e.rows;
@@ -1005,7 +1004,7 @@ __global__ void __launch_bounds__(ET, 1)
     uint8_t* rows = qs + rings.q * qtile + warp * 8192;    // 32 rows of 256 bytes
     auto piece = [&](int tr, int p) { return tr * 256 + ((p ^ (tr & 7)) << 4); };
     // Whole blocks of 32 tokens that are all there go by offsets kept in
-    // registers (9 instructions in 16 bytes would be spent on them otherwise).
+    // registers.
     const bool fast = a.fast_y && busy && token0 + 32 <= cnt && l != a.count;
     uint32_t offset[16];
 #pragma unroll
@@ -1074,7 +1073,7 @@ __global__ void __launch_bounds__(ET, 1)
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) {
             const int j = j0 + 32 / CH * k;
-            if (j < r16) v[k].store(to + spot(j), r16 * 2 * (CB > 64 ? CB : 64));
+            if (j < r16) v[k].store(to + spot(j), r16 * 2 * CB);
           }
         }
       }
@@ -1163,7 +1162,7 @@ __global__ void __launch_bounds__(ET, 1)
               for (int k = 0; k < r16 / 16; ++k) {
                 // descriptors' addresses count 16 bytes
                 tc_mma_f16(d, ha + (uint64_t)(((ph * kb + k / 4) * XT_BYTES + (k % 4) * 32) >> 4),
-                           qa + (uint64_t)((pw * r16 * 2 * (CB > 64 ? CB : 64) + k * 2048) >> 4), idesc, !first);
+                           qa + (uint64_t)((pw * r16 * 2 * CB + k * 2048) >> 4), idesc, !first);
                 first = false;
               }
             }
@@ -1379,10 +1378,8 @@ struct OuterPair {             // column blocks [0, split) are the first's, the 
   const uint8_t* u[2];
   int split;
 };
-// Resident CTAs take the (chunk, column block) pairs in turn: those that run at
-// a time read neighbouring columns of the same rows (each CTA a run of chunks
-// of one block took every row's piece from another DRAM page: 2.6 TB/s), and
-// all get long and short chunks alike.  Warps: the stages', one to
+// Resident CTAs take the (chunk, column block) pairs in turn, so that all get
+// long and short chunks alike.  Warps: the stages', one to
 // multiply, others that write a pair's sums while the next is multiplied into
 // the other half of TMEM (where two sets of accumulators fit); each goes
 // through the pairs by itself.
@@ -1485,9 +1482,7 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
       }
     } else if (warp == MW) {
       if (lane == 0) {
-        // The descriptors' addresses count 16 bytes: built once, stages and
-        // steps are added (built for each of 24 products a stage they took
-        // 2 us of this one thread).
+        // descriptors' addresses count 16 bytes: stages and steps are added to them
         const uint64_t x0 = make_sw128_desc(smem_u32(sm), 8192, 1024);
         const uint64_t u0 = make_sw128_desc(smem_u32(sm) + PX * H * XB, 16, 1024);
         const int up = r16 * 128 >> 4;
