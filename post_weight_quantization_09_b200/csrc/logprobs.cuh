@@ -13,6 +13,8 @@
 // |x| 2^-26 from log2 e's own rounding.
 #pragma once
 
+#include <type_traits>
+
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -368,8 +370,7 @@ struct Finish {
     log_s = low ? logf(p.s) : log2f(p.s);
   }
   __device__ __forceinline__ bool empty() const { return p.T == NEG_INF && p.s == 0.f; }   // no logit above -inf
-  __device__ __forceinline__ float given(int v) const {
-    const float f = to_f32(x[v]);
+  __device__ __forceinline__ float given(float f) const {
     if (low) return empty() ? NEG_INF : (f - p.T) - log_s;
     if (f < -1e38f) return f - LN2 * (p.T + log_s);      // times log2 e it may leave fp32
     return LN2 * (fmaf(f, LOG2E, -p.T) - log_s);
@@ -381,13 +382,12 @@ struct Finish {
     if (a.tokens) {
       const int tok = a.tokens[row];
       if (tok >= a.V || tok < -1) record_status(QUIP_ERR_ARG);
-      a.logprob[row] = tok >= 0 && tok < a.V ? given(tok) : 0.f;
+      a.logprob[row] = tok >= 0 && tok < a.V ? given(to_f32(x[tok])) : 0.f;
     }
   }
   __device__ __forceinline__ void write_top(const Args& a, int64_t row, int at, unsigned long long c) const {
-    const int v = (int)~(uint32_t)c;
-    a.top_ids[row * a.k + at] = v;
-    a.top_values[row * a.k + at] = given(v);
+    a.top_ids[row * a.k + at] = (int)~(uint32_t)c;
+    a.top_values[row * a.k + at] = given(key_value((uint32_t)(c >> 32)));
   }
 };
 
@@ -527,23 +527,39 @@ __global__ void __launch_bounds__(NT)
   const float ge = g_entropy ? g_entropy[row] : 0.f;
   const float l = lse[row];
   const float H = ge != 0.f ? entropy[row] : 0.f;
-  const bool zero = (g == 0.f && ge == 0.f) || l == NEG_INF;
-  // -g p - ge p (ln p + H) = p (c0 + c1 ln p)
-  const float c0 = -g - ge * H, c1 = -ge;
-  auto one = [&](float f, int v) {
-    const float lnp = max_nan(f - l, -200.f);            // p = 0 below
-    float r = ex2(lnp * LOG2E) * fmaf(c1, lnp, c0);
-    if (v == tok) r += g;
-    return r;
-  };
   const int v0 = seg * grad_cols<TX>(), v1 = min(V, v0 + grad_cols<TX>());
   const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(d)) & 15) == 0;
-  if (vec) {
+  if ((g == 0.f && ge == 0.f) || l == NEG_INF) {
+    for (int v = v0 + N * threadIdx.x; v < v1; v += N * NT) {
+      if (vec && v + N <= v1) *reinterpret_cast<uint4*>(d + v) = make_uint4(0u, 0u, 0u, 0u);
+      else
+        for (int i = v; i < min(v + N, v1); ++i) d[i] = from_f32<TX>(0.f);
+    }
+    return;
+  }
+  // -g p - ge p (ln p + H) = p (c0 + c1 ln p); without an entropy gradient
+  // (c1 = 0) p alone, and no care for p = 0 times ln p = -inf
+  const float c0 = -g - ge * H, c1 = -ge;
+  auto write = [&](auto entropy_too) {
+    auto one = [&](float f) {
+      if constexpr (decltype(entropy_too)::value) {
+        const float lnp = max_nan(f - l, -200.f);          // p = 0 below
+        return ex2(lnp * LOG2E) * fmaf(c1, lnp, c0);
+      } else {
+        return ex2((f - l) * LOG2E) * c0;
+      }
+    };
+    auto scalar = [&](int v) { d[v] = from_f32<TX>(one(to_f32(x[v])) + (v == tok ? g : 0.f)); };
+    if (!vec) {
+      // rows whose logits and gradients do not both start on 16 bytes
+      for (int v = v0 + threadIdx.x; v < v1; v += NT) scalar(v);
+      return;
+    }
     uint4 u[GRAD_VECS];
 #pragma unroll
     for (int j = 0; j < GRAD_VECS; ++j) {
       const int v = v0 + (threadIdx.x + j * NT) * N;
-      u[j] = v + N <= v1 && !zero ? *reinterpret_cast<const uint4*>(x + v) : make_uint4(0u, 0u, 0u, 0u);
+      u[j] = v + N <= v1 ? *reinterpret_cast<const uint4*>(x + v) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int j = 0; j < GRAD_VECS; ++j) {
@@ -553,16 +569,22 @@ __global__ void __launch_bounds__(NT)
         alignas(16) TX o[N];
         Vec<TX>::unpack(u[j], f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = from_f32<TX>(zero ? 0.f : one(f[i], v + i));
+        for (int i = 0; i < N; ++i) f[i] = one(f[i]);
+        if ((unsigned)(tok - v) < (unsigned)N) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (v + i == tok) f[i] += g;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = from_f32<TX>(f[i]);
         *reinterpret_cast<uint4*>(d + v) = *reinterpret_cast<const uint4*>(o);
       } else {
-        for (int i = v; i < v1; ++i) d[i] = from_f32<TX>(zero ? 0.f : one(to_f32(x[i]), i));
+        for (int i = v; i < v1; ++i) scalar(i);
       }
     }
-  } else {
-    // rows whose logits and gradients do not both start on 16 bytes
-    for (int v = v0 + threadIdx.x; v < v1; v += NT) d[v] = from_f32<TX>(zero ? 0.f : one(to_f32(x[v]), v));
-  }
+  };
+  if (ge != 0.f) write(std::true_type{});
+  else write(std::false_type{});
 }
 
 }  // namespace lp
