@@ -416,7 +416,8 @@ quip_status quip_qmatvec(const quip_transform* tf, const uint32_t* packed, int64
  *           status word and nothing is written.
  *   ws    : quip_adapter_workspace_size(..., 0) bytes, none (NULL) where that
  *           is 0 (small batches) or where both a plan and h are given.
- * Sums are fp32; y is rounded once.  1 <= r <= QUIP_ADAPTER_MAX_RANK,
+ * Sums are fp32; y is rounded once.  A token whose x, h or product is not
+ * finite gets NaN or infinities in its own rows, no other token does.  1 <= r <= QUIP_ADAPTER_MAX_RANK,
  * 1 <= count <= QUIP_ADAPTER_MAX_COUNT, T <= 2^22, n, m <= 2^24; T = 0 does
  * nothing.  Any alignment and strides; 16-byte aligned rows of bf16 are
  * fastest.

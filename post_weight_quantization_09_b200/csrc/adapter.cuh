@@ -8,9 +8,13 @@
 //   d_down_l = sum_t dh_t x_t^T,  d_up_l = s_l sum_t h_t dy_t^T
 // are one kernel for an outer product summed over an adapter's tokens.
 //
-// The arithmetic is 4 T r (n + m) flops forward and backward together with
-// the activations and the factors of the adapters in use to read: at ranks up
-// to 64 the bytes bound it.
+// Forward and gradient of the activations take 2 T r (n + m) flops each, the
+// weight gradients as much; at ranks up to 64 the bytes of x, y and dy bound
+// all of them (rank 64 does 64 flops a byte, the GPU 250).
+//
+// By the number of tokens (adapter_direct in quip_api.cu): few go straight
+// from ids, a cluster per token; more are grouped by adapter first (the plan)
+// and taken in tiles of 128 tokens on the tensor cores.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -70,6 +74,8 @@ __host__ __device__ inline PlanView plan_view(void* plan, int64_t T, int64_t cou
   return v;
 }
 
+// Latency bound (7 us for 4096 tokens, 11 for 8192); a model makes it once per
+// batch for all its layers.
 // One CTA of 32 warps: a stable counting sort of the tokens by adapter, each
 // warp a contiguous share of the tokens with counters of its own (a warp's
 // equal ids are ranked by match.any), then the tables.  Shared memory:
@@ -298,7 +304,9 @@ __device__ __forceinline__ bool plan_ok(const PlanView& pv, int T, int count) {
 // each thread's first columns of Q and the base for the expand.  Every CTA
 // stores its partial h into all others' shared memory and, past one cluster
 // barrier, adds them up in rank order.  fp32 on the CUDA cores; any type,
-// rank and alignment.
+// rank and alignment.  4096 x 4096, rank 16: 5.8 us for one token (9.2 us with
+// x staged in shared memory and Q asked for after h); 4096 -> 11008, 64 tokens
+// over 32 adapters: 13.1 us (21.6 us; 22 MB).
 constexpr int VT = 256;                        // threads per CTA
 constexpr int EARLY = 16;                      // rows of Q asked for at once
 constexpr int TOKEN_CTAS = 8;                  // of a cluster, at most
@@ -436,7 +444,8 @@ __global__ void __launch_bounds__(VT, sizeof(TW) == 2 ? 4 : 2)
 // For the types and ranks that the tensor-core tiles do not take: the plan's
 // tiles of up to SMALL tokens of one adapter, one cluster each.  Its CTAs
 // share n, exchange their partial h through distributed shared memory
-// (summed in rank order by each), and share m.  fp32 on the CUDA cores.
+// (summed in rank order by each), and share m.  fp32 on the CUDA cores; the
+// factors come from L2 once per 8 tokens, which bounds it.
 constexpr int NTOK = SMALL, VROWS = 4, VCOLS = 1024;   // tokens; rows of P per warp task; columns of x staged at once
 inline size_t vec_smem(int r) {
   return sizeof(float) * ((size_t)NTOK * VCOLS + (size_t)(VT / 32) * NTOK * VROWS + 2 * (size_t)NTOK * up4(r));
@@ -596,7 +605,9 @@ __global__ void __launch_bounds__(VT)
 // h[token][j] over its 64-column blocks with tcgen05 (M = 128 tokens, N = r,
 // both operands K-major), the partial sums meet through distributed shared
 // memory (each CTA adds up a share of the tokens, in rank order), h goes to
-// memory.
+// memory.  8192 tokens of 11008 bf16 columns, rank 32: 39 us, 4.6 TB/s (27 us
+// at the measured copy rate); 4096 of 8192, rank 64: 25 us, mostly the start
+// and the cluster's sum.
 //
 // Expand: resident CTAs, each an equal run of the (tile, column block) pairs:
 // D[token][column] = h Q (M = 128 tokens, N = the block's columns, K = r, Q
@@ -606,6 +617,9 @@ __global__ void __launch_bounds__(VT)
 // neighbouring lanes, adds a row's products there, and sends the sums out as
 // the base came, while the other groups' rows are on their way.  The sides
 // meet at mbarriers only (tile of Q there, accumulator full, accumulator read).
+// 4096 tokens x 28672 bf16 columns, rank 64: 106 us, 4.4 TB/s (72 us at the
+// copy rate; 140 us with two CTAs an SM that met at every block, 200 us with
+// each lane on its own row's bytes).  The latency of a warp's chain bounds it.
 //
 // Types: a bf16 value is one operand piece, an fp32 value three (split3), and
 // the products of pieces of order 2 and below are formed: fp32 operands keep
@@ -1311,6 +1325,9 @@ __global__ void __launch_bounds__(OT) k_adapter_outer(const __grid_constant__ Ou
 // cycles whatever N.  (OuterBlocks: which pieces go together.)  The pieces are
 // made once, K-major and swizzled as the tensor core reads them
 // (k_adapter_pieces), so that a stage takes them by one bulk copy.
+// 8192 tokens, 4096 and 11008 columns, rank 32: 80 us for both sums, 3.1 TB/s
+// (38 us at the copy rate); 100 us with a product per piece, 150 us with u cut
+// into pieces by every CTA, 3700 us on the CUDA cores with all else.
 __host__ __device__ inline int64_t max_subs(int64_t T, int64_t count) { return T / SUB + (count < T ? count : T) + 1; }
 __host__ __device__ inline int u_bytes(int r16) { return 3 * r16 * 128; }    // of SUB tokens
 

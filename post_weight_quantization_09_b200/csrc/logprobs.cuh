@@ -440,6 +440,13 @@ __device__ __forceinline__ void close_row(Running& r, const Slice<TX>& sl, RowSh
 
 // One cluster per row (one CTA where the rows fill the GPU, up to 8 where
 // they do not), each CTA a slice of it; the first CTA combines.
+// 4096 x 32000 bf16: 52 us, 5.0 TB/s, 63 us with five alternatives; 2047 x
+// 50257 fp32: 74 us, 5.6 TB/s; 64 x 128000 bf16: 7.3 us, 13.7 us with twenty
+// (a chain of barriers and L2 loads); one row of 32000: 6.1 us.  A bf16 logit
+// costs six to seven instructions and an ex2, which with the loads' latency
+// bound it; 256 threads with five CTAs an SM were as fast as 128 with ten, and
+// resident CTAs behind a ring of bulk copies slower by 3 us (no alternatives)
+// to 20 us.
 template <typename TX, bool TOP>
 __global__ void __launch_bounds__(NT, 5) k_logprobs(const TX* __restrict__ logits, const __grid_constant__ Args a) {
   constexpr int N = Vec<TX>::N;
@@ -494,7 +501,9 @@ __global__ void __launch_bounds__(NT, 5) k_logprobs(const TX* __restrict__ logit
 }
 
 // d_logits[v] = g (1[v = tok] - p_v) - ge p_v (ln p_v + H), p_v = exp(x_v - lse).
-// Elementwise: one read and one write per logit bound it.  A row with g = 0
+// Elementwise: one read and one write per logit bound it (4096 x 32000 bf16:
+// 84.5 us, 6.2 TB/s; with the token's and the entropy's terms in every element
+// 91 us).  A row with g = 0
 // (or no token) and ge = 0 is 0 without its logits being looked at, as is a
 // row with no logit above -inf.
 template <typename TX>
