@@ -1305,7 +1305,7 @@ __global__ void __launch_bounds__(OT) k_adapter_outer(const __grid_constant__ Ou
     }
   }
   if (left <= 0) return;
-  const float k = a.scale ? a.scale[l] : 1.f;
+  const float k = a.scale && cnt > 0 ? a.scale[l] : 1.f;      // an adapter without tokens: 0, whatever its scale
   float* out = chunk.z < 0 ? a.out + (int64_t)l * a.r * a.width : a.partial + (int64_t)chunk.z * a.r * a.width;
   const bool add = chunk.z < 0 && a.accumulate;
   for (int j = 0; j < OROWS && j0 + j < a.r; ++j)
@@ -1554,7 +1554,7 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
       const int half = (warp - MW - 1) / 4, n = items, c = c0 + 128 * half + 32 * (warp % 4) + lane;
       if (steps > 0) ok = ok && mbar_wait(&ready[n % sets], (uint32_t)((n / sets) & 1));
       tc_fence_after();
-      const float k = a.scale ? a.scale[l] : 1.f;
+      const float k = a.scale && steps > 0 ? a.scale[l] : 1.f;      // an adapter without tokens: 0, whatever its scale
       float* out = chunk.z < 0 ? a.out + (int64_t)l * r * a.width : a.partial + (int64_t)chunk.z * r * a.width;
       const bool add = chunk.z < 0 && a.accumulate;
       const uint32_t at = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + (uint32_t)(n % sets * (TCOLS / 2) + half * blk.total * r16);

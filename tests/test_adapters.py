@@ -253,6 +253,38 @@ def test_strided_rows(clean, T, pad, x, y):
 
 
 @gpu
+@pytest.mark.parametrize("T,ld", [(4, 2 ** 30 + 8), (300, 2 ** 23 + 8)])
+def test_row_offsets_past_32_bits(clean, T, ld):
+    c = Case(T, 264, 136, 16, 3)
+
+    def far(t):
+        return torch.empty((T - 1) * ld + t.shape[1], dtype=t.dtype, device="cuda").as_strided(t.shape, (ld, 1)).copy_(t)
+    c.x, c.y, c.base, c.dy, c.dx, c.dx_base = (far(t) for t in (c.x, c.y, c.base, c.dy, c.dx, c.dx_base))
+    c.apply()
+    c.check_apply()
+    c.backward()
+    c.check_backward()
+
+
+@gpu
+@pytest.mark.parametrize("T,r", [(3, 128), (300, 128), (300, 256)])
+def test_factor_offsets_past_32_bits(clean, T, r):
+    # the last of 1024 adapters starts behind 2^31 values; the others are never read
+    n = 2 ** 31 // (1023 * r) + 8 & ~7
+    c = Case(T, n, n, r, 1, ids="one")
+    down, up = (torch.empty(1024, r, n, dtype=B, device="cuda") for _ in range(2))
+    d_down, d_up = (torch.full((1024, r, n), float("nan"), device="cuda") for _ in range(2))
+    down[-1], up[-1] = c.down[0], c.up[0]
+    scale, ids = c.scale.repeat(1024), torch.full_like(c.ids, 1023)
+    Q.quip_adapter_apply(c.x, ids, down, up, scale, c.y, base=c.base, h=c.h)
+    c.check_apply()
+    Q.quip_adapter_backward(c.x, c.dy, ids, down, up, scale, c.h, dx=c.dx, dx_base=c.dx_base, d_down=d_down, d_up=d_up)
+    c.d_down, c.d_up, c.acc = d_down[-1:], d_up[-1:], 0.0
+    c.check_backward()
+    assert not d_down[:-1].any() and not d_up[:-1].any()
+
+
+@gpu
 def test_unaligned_tensors(clean):
     # every operand one element off its 16-byte boundary
     for T in (4, 300):
@@ -305,6 +337,21 @@ def test_parts_of_the_gradient_and_accumulation(clean, T):
     assert torch.equal(d, du)
     with pytest.raises(ValueError):
         Q.quip_adapter_backward(c.x, c.dy, c.ids, c.down, c.up, c.scale, None, d_up=d)
+
+
+@gpu
+@pytest.mark.parametrize("r", [16, 160])
+@pytest.mark.parametrize("T", [0, 6, 300])
+@pytest.mark.parametrize("accumulate", [0.0, 3.0])
+def test_unused_adapters_may_hold_anything(clean, T, r, accumulate):
+    c = Case(T, 256, 192, r, 5)
+    c.ids[:] = torch.as_tensor(np.where(np.arange(T) % 3 == 0, -1, 2).astype(np.int32))
+    for t in (c.down, c.up, c.scale):
+        t[[0, 1, 3, 4]] = float("nan")
+    c.apply()
+    c.check_apply()
+    c.backward(accumulate)
+    c.check_backward()
 
 
 @gpu

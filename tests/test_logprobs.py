@@ -284,6 +284,21 @@ def test_gradient_matches_oracle(clean, T, V, pad, inplace, dtype):
 
 
 @gpu
+def test_row_offsets_past_32_bits(clean):
+    T, V, ld = 4, 5000, 2 ** 30 + 8
+    x, tokens = _logits(T, V, torch.bfloat16, 17)
+    far = torch.empty((T - 1) * ld + V, dtype=torch.bfloat16, device="cuda").as_strided((T, V), (ld, 1)).copy_(x)
+    got, want = _run(far, tokens, 9), _run(x, tokens, 9)
+    _check(x, tokens, 9, got)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g = torch.linspace(-1, 1, T, device="cuda")
+    d = torch.empty_like(x)
+    for logits, out in ((x, d), (far, far)):
+        Q.quip_logprobs_backward(logits, tokens, want[2], out, g_logprob=g, g_entropy=g, entropy=want[1])
+    assert torch.equal(far, d)
+
+
+@gpu
 def test_gradient_parts_may_be_absent(clean):
     x, tokens = _logits(3, 500, torch.float32, 8)
     _, H, lse, _, _ = _run(x, tokens, 0)
