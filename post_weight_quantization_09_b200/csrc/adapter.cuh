@@ -1001,7 +1001,9 @@ __global__ void __launch_bounds__(ET, 1)
   }
   uint32_t tmem = 0;
   bool ok = true, started = false;             // the wait for h, and TMEM
-  int done = 0;                                // blocks multiplied so far: accumulator, phase and tile of the next
+  int done = 0;                                // blocks multiplied so far: accumulator and phase of the next
+  int ring = 0;                                // the multiplying warp's next tile of Q, and its phase
+  uint32_t ring_phase = 0;
   const uint32_t idesc = make_idesc_bf16(TILE, CB, 0, 1);
   for (int64_t w = w0; w < w1;) {
     const int2 tile = pv.tiles[w / blocks];
@@ -1018,14 +1020,16 @@ __global__ void __launch_bounds__(ET, 1)
     uint8_t* rows = qs + rings.q * qtile + warp * 8192;    // 32 rows of 256 bytes
     auto piece = [&](int tr, int p) { return tr * 256 + ((p ^ (tr & 7)) << 4); };
     // Whole blocks of 32 tokens that are all there go by offsets kept in
-    // registers.
+    // registers, others by tok's, four rounds at once.
     const bool fast = a.fast_y && busy && token0 + 32 <= cnt && l != a.count;
     uint32_t offset[16];
 #pragma unroll
     for (int v = 0; v < 16; ++v)
       offset[v] = fast ? (uint32_t)(tok[token0 + 2 * v + lane / 16] * (a.ldy / EV)) + lane % 16 : 0u;
+    const int rounds = busy ? (min(32, cnt - token0) + 1) / 2 : 0;
     auto fill_rows = [&](int i) {
-      if (fast && i < steps && (b0 + i + 1) * CB <= a.m) {
+      if (i >= steps || !a.base || !busy) return;
+      if (fast && (b0 + i + 1) * CB <= a.m) {
         const uint4* from = reinterpret_cast<const uint4*>(a.base) + (b0 + i) * (CB / EV);
         const uint32_t to = smem_u32(rows) + lane / 16 * 256;
 #pragma unroll
@@ -1034,14 +1038,31 @@ __global__ void __launch_bounds__(ET, 1)
                            to + v * 512 + (((lane % 16) ^ ((2 * v + lane / 16) & 7)) << 4)),
                        "l"(from + offset[v])
                        : "memory");
-      } else if (i < steps && a.base && busy) {
+      } else if (sizeof(TY) == 4 && !a.vec_y) {
+        // fp32 at any alignment: a lane's columns are lane and lane + 32
+        const int c = (b0 + i) * CB + lane;
+        const uint32_t to = smem_u32(rows) + lane % 4 * 4;
+#pragma unroll 8
+        for (int tr = 0; tr < 32; ++tr) {
+          const int t = tok[token0 + tr];
+          if (t < 0) break;                    // the tile's tokens come first
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (c + 32 * h < a.m)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + piece(tr, 8 * h + lane / 4)),
+                           "l"(a.base + t * a.ldb + c + 32 * h)
+                           : "memory");
+        }
+      } else {
         const int c = (b0 + i) * CB + col, left = a.m - c;
         if (a.vec_y && (b0 + i + 1) * CB <= a.m) {
-#pragma unroll 4
-          for (int v = 0; v < 16; ++v) {
-            const int tr = 2 * v + lane / 16;
-            const int64_t t = tok[token0 + tr];
-            if (t >= 0) cp16(rows + piece(tr, lane % 16), a.base + t * a.ldb + c, true);
+          for (int v0 = 0; v0 < rounds; v0 += 4) {
+            int t[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) t[v] = tok[token0 + 2 * (v0 + v) + lane / 16];
+#pragma unroll
+            for (int v = 0; v < 4; ++v)        // zeros where there is no token
+              cp16(rows + piece(2 * (v0 + v) + lane / 16, lane % 16), a.base + max(t[v], 0) * a.ldb + c, t[v] >= 0);
           }
           return;
         }
@@ -1158,28 +1179,35 @@ __global__ void __launch_bounds__(ET, 1)
     __syncthreads();
     if (warp == EW + QW) {
       if (lane == 0) {
+        // descriptors' addresses (low 14 bits) count 16 bytes: pieces and steps
+        // are added to them
         const uint64_t ha = make_sw128_desc(smem_u32(sm), 16, 1024);
+        const int ks = r16 / 16;
         for (int i = 0; i < steps && ok; ++i) {
-          const int n = done + i, b = n % ACCS, s = n % rings.q;
-          ok = mbar_wait(&there[s], (uint32_t)((n / rings.q) & 1));
+          const int n = done + i, b = n % ACCS;
+          ok = mbar_wait(&there[ring], ring_phase);
           if (n >= ACCS) ok = ok && mbar_wait(&read[b], (uint32_t)((n / ACCS - 1) & 1));
           if (!ok) break;
           tc_fence_after();
-          const uint64_t qa = make_sw128_desc(smem_u32(qs + s * qtile), r16 * 128, 1024);
+          const uint64_t qa = make_sw128_desc(smem_u32(qs + ring * qtile), r16 * 128, 1024);
           const uint32_t d = tmem + (uint32_t)(b * CB);
-          bool first = true;
 #pragma unroll
           for (int ph = NP - 1; ph >= 0; --ph)           // the small terms first
 #pragma unroll
             for (int pw = PW - 1; pw >= 0; --pw) {
               if (ph + pw > 2) continue;
-              for (int k = 0; k < r16 / 16; ++k) {
-                // descriptors' addresses count 16 bytes
-                tc_mma_f16(d, ha + (uint64_t)(((ph * kb + k / 4) * XT_BYTES + (k % 4) * 32) >> 4),
-                           qa + (uint64_t)((pw * r16 * 2 * CB + k * 2048) >> 4), idesc, !first);
-                first = false;
+              const bool more = ph != NP - 1 || pw != (PW - 1 < 3 - NP ? PW - 1 : 3 - NP);     // not the first pair
+              uint64_t hd = ha + (uint64_t)(ph * kb * XT_BYTES >> 4);
+              uint64_t qd = qa + (uint64_t)(pw * r16 * 2 * CB >> 4);
+              for (int k = 0; k < ks; k += 4, hd += XT_BYTES >> 4, qd += 4 * 2048 >> 4) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  if (kk == 0 || k + kk < ks)
+                    tc_mma_f16(d, hd + (uint64_t)(kk * 32 >> 4), qd + (uint64_t)(kk * 2048 >> 4), idesc,
+                               more || kk > 0 || k > 0);
               }
             }
+          if (++ring == rings.q) ring = 0, ring_phase ^= 1u;
           tc_commit(&full[b]);
         }
       }
@@ -1218,6 +1246,31 @@ __global__ void __launch_bounds__(ET, 1)
 #pragma unroll
           for (int v = 0; v < 16; ++v)
             to[offset[v]] = *reinterpret_cast<const uint4*>(rows + piece(2 * v + lane / 16, lane % 16));
+        } else if (a.vec_y && busy && ok && (b0 + i + 1) * CB <= a.m) {
+          const int c = (b0 + i) * CB + col;
+          for (int v0 = 0; v0 < rounds; v0 += 4) {
+            int t[4];
+            uint4 u[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              t[v] = tok[token0 + 2 * (v0 + v) + lane / 16];
+              u[v] = *reinterpret_cast<const uint4*>(rows + piece(2 * (v0 + v) + lane / 16, lane % 16));
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (t[v] >= 0) *reinterpret_cast<uint4*>(a.y + t[v] * a.ldy + c) = u[v];
+          }
+        } else if (sizeof(TY) == 4 && !a.vec_y && busy && ok) {
+          const int c = (b0 + i) * CB + lane;
+#pragma unroll 8
+          for (int tr = 0; tr < 32; ++tr) {
+            const int t = tok[token0 + tr];
+            const float f0 = *reinterpret_cast<const float*>(rows + piece(tr, lane / 4) + lane % 4 * 4);
+            const float f1 = *reinterpret_cast<const float*>(rows + piece(tr, 8 + lane / 4) + lane % 4 * 4);
+            TY* y = a.y + t * a.ldy + c;
+            if (t >= 0 && c < a.m) put(y, f0);
+            if (t >= 0 && c + 32 < a.m) put(y + 32, f1);
+          }
         } else if (busy && ok) {
           const int c = (b0 + i) * CB + col, left = a.m - c;
 #pragma unroll 4

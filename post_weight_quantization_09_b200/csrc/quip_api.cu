@@ -1998,7 +1998,7 @@ template <typename TX, typename TW, typename TY>
 cudaError_t adapter_tc(const ad::ApplyArgs<TX, TW, TY>& a, void* plan, cudaStream_t st) {
   const bool vec_y = rows_of_eight(a.y, a.T > 1 ? a.ldy : 8, sizeof(TY)) &&
                      (!a.base || rows_of_eight(a.base, a.T > 1 ? a.ldb : 8, sizeof(TY)));
-  const bool fast_y = vec_y && a.base && (a.T == 1 || a.ldb == a.ldy) &&
+  const bool fast_y = vec_y && (!a.base || a.T == 1 || a.ldb == a.ldy) &&
                       a.T * a.ldy * (int64_t)sizeof(TY) / 16 < (int64_t(1) << 31);
   const ad::ApplyArgs<TX, TW, float> s{a.x, a.ldx, a.P, nullptr, a.scale, nullptr, 0, nullptr, 0, a.h, a.T, a.n, a.m,
                                        a.r, a.count, a.h_scaled, a.vec_x, a.vec_p, false, false, false};
