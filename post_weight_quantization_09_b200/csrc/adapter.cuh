@@ -619,7 +619,11 @@ __global__ void __launch_bounds__(VT)
 // meet at mbarriers only (tile of Q there, accumulator full, accumulator read).
 // 4096 tokens x 28672 bf16 columns, rank 64: 106 us, 4.4 TB/s (72 us at the
 // copy rate; 140 us with two CTAs an SM that met at every block, 200 us with
-// each lane on its own row's bytes).  The latency of a warp's chain bounds it.
+// each lane on its own row's bytes).  By clocks read in the kernel the
+// multiplying warp bounds it: of 2450 clocks a block it spends 1180 on its
+// eight products, 620 on the fence and the commit around them, 290 waiting;
+// a group of row warps needs a block's rows for 5100 of 4 x 2450.  16 tokens
+// to a tile and fp32 rows: 1100 of 1900, before the products were one loop.
 //
 // Types: a bf16 value is one operand piece, an fp32 value three (split3), and
 // the products of pieces of order 2 and below are formed: fp32 operands keep
@@ -1191,20 +1195,20 @@ __global__ void __launch_bounds__(ET, 1)
           tc_fence_after();
           const uint64_t qa = make_sw128_desc(smem_u32(qs + ring * qtile), r16 * 128, 1024);
           const uint32_t d = tmem + (uint32_t)(b * CB);
-#pragma unroll
+          // one product in the code: unrolled, 512 tokens over 32 adapters took
+          // 63 us (59 now), 4096 of rank 64 the same
+          bool more = false;
+#pragma unroll 1
           for (int ph = NP - 1; ph >= 0; --ph)           // the small terms first
-#pragma unroll
-            for (int pw = PW - 1; pw >= 0; --pw) {
-              if (ph + pw > 2) continue;
-              const bool more = ph != NP - 1 || pw != (PW - 1 < 3 - NP ? PW - 1 : 3 - NP);     // not the first pair
+#pragma unroll 1
+            for (int pw = min(PW - 1, 2 - ph); pw >= 0; --pw) {
               uint64_t hd = ha + (uint64_t)(ph * kb * XT_BYTES >> 4);
               uint64_t qd = qa + (uint64_t)(pw * r16 * 2 * CB >> 4);
-              for (int k = 0; k < ks; k += 4, hd += XT_BYTES >> 4, qd += 4 * 2048 >> 4) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  if (kk == 0 || k + kk < ks)
-                    tc_mma_f16(d, hd + (uint64_t)(kk * 32 >> 4), qd + (uint64_t)(kk * 2048 >> 4), idesc,
-                               more || kk > 0 || k > 0);
+#pragma unroll 1
+              for (int k = 0; k < ks; ++k, qd += 2048 >> 4) {
+                tc_mma_f16(d, hd, qd, idesc, more);
+                hd += k % 4 == 3 ? (XT_BYTES - 96) >> 4 : 32 >> 4;
+                more = true;
               }
             }
           if (++ring == rings.q) ring = 0, ring_phase ^= 1u;
