@@ -117,12 +117,13 @@ template <> struct Vec<__nv_bfloat16> {
 constexpr float LOW_T = 4096.f;
 
 // (T, s, w) of a part of a row.  T = -inf: no logit that 2^(t - T) can serve
-// (none above -inf, or all near the type's lowest value), s = w = 0, or NaN
+// (none above LEAST_T, Running below), s = w = 0, or NaN
 // where it met one.
 struct Part {
   float T, s, w;
   __device__ __forceinline__ void raise(float to) {     // to >= T
-    const float d = T == NEG_INF ? 0.f : T - to;
+    // 2^-200 is 0 in fp32; a longer way down times s may leave fp32
+    const float d = T == NEG_INF ? 0.f : max_nan(T - to, -200.f);
     const float f = ex2(d);
     w = f * fmaf(d, s, w);
     s *= f;
@@ -147,10 +148,16 @@ __device__ __forceinline__ Part warp_combine(Part p) {
 // maximum only once that is SLACK above it (2^(t - T) has room; the entropy's
 // log2 s and w / s then share up to SLACK, half a step of which is small):
 // most rounds then cost a comparison.
-constexpr float SLACK = 8.f;
+//
+// T does not follow a maximum of LEAST_T and below (masks of large finite
+// values): the rounding of such a T is no longer small beside 1 (half a step
+// of 2^31 is 128, and 2^128 is infinite).  Those logits are held as those of
+// -inf are, and count 0 beside any other; a row of nothing else is sum_low's.
+constexpr float SLACK = 8.f, LEAST_T = -1e6f;
 struct Running {
   float m = NEG_INF;
   Part p{NEG_INF, 0.f, 0.f};
+  float raise_at = LEAST_T;
   // A logit of -inf (a barred token, padding) has e = 0, but t - T = -inf
   // would make e (t - T) NaN: logits are held at a value whose exponential is
   // 0 in fp32, at least 100 below T's after its rounding to bf16 too
@@ -159,8 +166,9 @@ struct Running {
   // `top` is the maximum of the logits about to be added
   __device__ __forceinline__ void raise(float top) {
     m = fmaxf(m, top);
-    if (m * LOG2E > p.T + SLACK) {
+    if (m * LOG2E > raise_at) {
       p.raise(m * LOG2E);
+      raise_at = p.T + SLACK;
       floor = m - fmaxf(200.f, fabsf(m) * 0.015625f);
       ref = -p.T;
     }

@@ -366,3 +366,56 @@ def test_score_of_a_quantized_output_layer(clean):
     with pytest.raises(ValueError):
         ql.score(x, tokens[:3])
     tf.close()
+
+
+# ------------------------------------------------------------------ finite masks
+
+def _masked(T, V, dtype, value, seed):
+    """Random rows with `value` at, row by row: half the entries, 99 in 100,
+    a stretch of up to 4096, all but one."""
+    x, tokens = _logits(T, V, dtype, seed)
+    g = torch.Generator().manual_seed(seed)
+    kind = (torch.arange(T) % 4)[:, None]
+    v, start = torch.arange(V)[None], torch.randint(0, max(V - 4096, V // 4), (T, 1), generator=g)
+    mask = torch.where(kind == 0, torch.rand(T, V, generator=g) < 0.5, torch.rand(T, V, generator=g) < 0.99)
+    mask = torch.where(kind == 2, (v >= start) & (v < start + 4096), mask) | (kind == 3)
+    mask[:, V // 2] = False
+    x.masked_fill_(mask.cuda(), value)
+    return x, tokens
+
+
+MASKS = [-1e9, -1e10, -1e12, -1e20, -1e30, -1e38, "half", "min"]
+
+
+def _mask_value(value, dtype):
+    return {"half": torch.finfo(dtype).min / 2, "min": torch.finfo(dtype).min}.get(value, value)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("value", MASKS)
+@pytest.mark.parametrize("T,V,k", [(1, 500, 3), (700, 500, 0), (700, 500, 5), (4, 32000, 8), (4, 128000, 20), (600, 9000, 2)])
+def test_finite_masks_count_nothing(clean, T, V, k, value, dtype):
+    x, tokens = _masked(T, V, dtype, _mask_value(value, dtype), T + V)
+    _check(x, tokens, k, _run(x, tokens, k))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("value", MASKS)
+def test_gradient_beside_finite_masks(clean, value, dtype):
+    T, V = 8, 9001
+    x, tokens = _masked(T, V, dtype, _mask_value(value, dtype), 5)
+    tokens.fill_(V // 2)
+    _, H, lse, _, _ = _run(x, tokens, 0)
+    g, ge = torch.linspace(-1, 1, T, device="cuda"), torch.linspace(0.5, 1.5, T, device="cuda")
+    d = torch.empty_like(x)
+    Q.quip_logprobs_backward(x, tokens, lse, d, g_logprob=g, g_entropy=ge, entropy=H)
+    x64, lse64, H64, g64, ge64 = (host(t) for t in (x, lse, H, g, ge))
+    want = O.token_logprobs_grad(x64, host(tokens).astype(np.int64), lse64, H64, g64, ge64)
+    logp = np.maximum(x64 - lse64[:, None], -1000.0)
+    # as in test_gradient_matches_oracle
+    size = np.exp(logp) * (np.abs(g64)[:, None] + ge64[:, None] * (H64[:, None] + np.abs(logp)))
+    tol = size * (8 + 3 * np.abs(logp)) * U + np.abs(want) * (U + torch.finfo(dtype).eps / 2 * (1 + 1e-3)) + 1e-37
+    tol[:, V // 2] += 2 * U * np.abs(g64)
+    assert np.all(np.abs(host(d) - want) <= tol), np.nanmax(np.abs(host(d) - want) / tol)
