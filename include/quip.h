@@ -499,7 +499,10 @@ quip_status quip_logprobs(const void* logits, int dtype, int64_t T, int64_t V, i
  *   d_logits[v] = g_logprob (1[v = tok] - p_v) - g_entropy p_v (ln p_v + entropy),
  * p_v = exp(x_v - lse); a row's token of -1 counts as g_logprob = 0.
  *   lse, entropy : device T fp32, as quip_logprobs wrote them (entropy is
- *                  needed with g_entropy only).
+ *                  needed with g_entropy only).  p carries the rounding of lse
+ *                  below |lse| = 256 (2^-17 of p at most); from there on it is
+ *                  made good from the row, at the cost of two more reads of
+ *                  it, where lse is this row's.
  *   g_logprob, g_entropy : device T fp32, the gradients of the row's logprob
  *                  and entropy; NULL counts as 0.  tokens is needed with
  *                  g_logprob.

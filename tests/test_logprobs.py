@@ -419,3 +419,95 @@ def test_gradient_beside_finite_masks(clean, value, dtype):
     tol = size * (8 + 3 * np.abs(logp)) * U + np.abs(want) * (U + torch.finfo(dtype).eps / 2 * (1 + 1e-3)) + 1e-37
     tol[:, V // 2] += 2 * U * np.abs(g64)
     assert np.all(np.abs(host(d) - want) <= tol), np.nanmax(np.abs(host(d) - want) / tol)
+
+
+# ------------------------------------------------------------------ gradients of rows far from 0
+
+def _far_rows(kind, dtype):
+    """(x, tokens) of 6 rows of logits whose log-sum-exp is far from 0."""
+    x, tokens = _logits(6, 9001, dtype, 21)
+    tokens[:] = torch.tensor([9001 // 2, 7, 0, -1, 9000, 4096])
+    if kind == "equal":                  # equal logits of any size, beside -inf
+        x = torch.where(torch.isfinite(x), torch.tensor([1e9, -1e9, 3e38, -3e38, 300.0, -5e5])[:, None].cuda(), x.float())
+    elif kind == "lowest":               # rows of the type's lowest value alone
+        x = torch.where(torch.isfinite(x), torch.finfo(dtype).min, x.float())
+    else:
+        x = x.float() + kind
+    x[torch.arange(6), tokens.long().clamp(min=0).cpu()] = x.amax(1)
+    return x.to(dtype), tokens
+
+
+def _far_check(x, tokens, g, ge, got):
+    """Against the oracle's own log-sum-exp and entropy: p loses 4 u + 3 u
+    |ln p| by its own arithmetic, and what lse lost: its computation (_check)
+    and at most half a step below 256, where the row itself is not looked at
+    again; else u of each of the few additions that correct it, ln V in size."""
+    x64, tok, V = host(x), host(tokens).astype(np.int64), x.shape[1]
+    far = np.abs(x64.max(1))
+    x64 = x64 - x64.max(1)[:, None]              # the gradient does not see it; FP64 would at 3e38
+    _, H, lse, _, _ = O.token_logprobs(x64, tok)
+    want = O.token_logprobs_grad(x64, tok, lse, H, host(g), host(ge))
+    logp = np.maximum(x64 - lse[:, None], -1000.0)
+    p = np.exp(logp)
+    spread = np.sum(p * -np.maximum(x64, -1000.0), 1)
+    rel = 4 * U + (V / 256 + 64) * U + 3 * U * spread
+    err = rel + 4 * U * (np.minimum(far, 256.0) + 2 * np.log(V) + 1)
+    err_h = rel + (2 * rel + 8 * U) * (spread + 1) + 8 * U * np.log(V)
+    g64 = np.where(tok >= 0, np.abs(host(g)), 0.0)[:, None]
+    ge64 = np.abs(host(ge))[:, None]
+    size = p * (g64 + ge64 * (H[:, None] + np.abs(logp)))
+    tol = size * ((8 + 3 * np.abs(logp)) * U + err[:, None]) + p * ge64 * (err + err_h)[:, None] + 1e-37
+    tol[np.arange(len(tok)), np.maximum(tok, 0)] += 2 * U * g64[:, 0]
+    tol += (np.abs(want) + tol) * (U + torch.finfo(x.dtype).eps / 2 * (1 + 1e-3))
+    off = np.abs(host(got) - want)
+    assert np.all(off <= tol), np.nanmax(off / tol)
+    assert np.all(host(got)[x64 == -np.inf] == 0)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", [100.0, -300.0, 5000.0, 1e6, -1e6, "equal", "lowest"])
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("entropy", [False, True])
+def test_gradient_far_from_zero(clean, kind, dtype, inplace, entropy):
+    x, tokens = _far_rows(kind, dtype)
+    keep = x.clone()
+    _, H, lse, _, _ = _run(x, tokens, 0)
+    g = torch.tensor([-1.0, 0.5, 2.0, 1.0, -0.25, 1.0], device="cuda")
+    ge = torch.linspace(-1, 1, 6, device="cuda") * entropy
+    out = x if inplace else torch.full_like(x, 7.0)
+    Q.quip_logprobs_backward(x, tokens, lse, out, g_logprob=g, g_entropy=ge if entropy else None, entropy=H)
+    _far_check(keep, tokens, g, ge, out)
+
+
+@gpu
+@pytest.mark.parametrize("V,pad,shift", [(1, 0, 0), (3, 1, 0), (257, 3, 1), (40000, 5, 3)])
+def test_gradient_far_from_zero_in_strided_rows(clean, V, pad, shift):
+    T = 5
+    x, tokens = _logits(T, V, torch.float32, V, scale=1.0)
+    x += 7000.0
+    buf, out = (torch.full((T, V + pad + shift), float("nan"), device="cuda") for _ in range(2))
+    view, d = buf[:, shift:shift + V], out[:, shift:shift + V]
+    view.copy_(x)
+    _, H, lse, _, _ = _run(view, tokens, 0)
+    g = torch.linspace(-1, 1, T, device="cuda")
+    Q.quip_logprobs_backward(view, tokens, lse, d, g_logprob=g, g_entropy=g, entropy=H)
+    _far_check(x, tokens, g, g, d)
+    out[:, shift:shift + V] = float("nan")
+    assert torch.isnan(out).all()
+
+
+@gpu
+def test_gradient_with_the_sum_of_a_larger_vocabulary(clean):
+    # the rows are shards: lse is that of the whole row, 1 more than the shard's
+    x, tokens = _logits(4, 5000, torch.float32, 9)
+    x += 5000.0
+    lse = _run(x, tokens, 0)[2] + 1.0
+    g = torch.ones(4, device="cuda")
+    d = torch.empty_like(x)
+    Q.quip_logprobs_backward(x, tokens, lse, d, g_logprob=g)
+    x64, lse64 = host(x), host(lse)
+    want = O.token_logprobs_grad(x64, host(tokens).astype(np.int64), lse64, np.zeros(4), np.ones(4), np.zeros(4))
+    p = np.exp(x64 - lse64[:, None])
+    tol = p * (8 + 3 * np.maximum(lse64[:, None] - x64, 0).clip(max=1000)) * U + 2 * U * np.abs(want) + 1e-37
+    assert np.all(np.abs(host(d) - want) <= tol)
