@@ -96,6 +96,14 @@ def _refuse(name, t, dtypes, shape, device, rows):
     raise ValueError(f"{name} must have contiguous rows that do not overlap" if rows else f"{name} must be contiguous")
 
 
+def _room(name: str, t: torch.Tensor, device: int):
+    """The address and bytes of a buffer that kernels write: contiguous memory
+    of ``device`` (the current one)."""
+    if t.get_device() != device or not t.is_contiguous():
+        _refuse(name, t, (t.dtype,), t.shape, device, False)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _row_stride(t: torch.Tensor) -> int:
     """Row stride of a 2-D tensor; one row has whatever stride its columns need."""
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
@@ -463,7 +471,7 @@ def quip_adapter_plan(ids: torch.Tensor, count: int, plan: Optional[torch.Tensor
     nb = _adapter_plan_bytes(T, count)
     if plan is None:
         plan = _scratch(nb, stream)
-    L.check(load().quip_adapter_plan(i, T, count, plan.data_ptr(), plan.numel(), _raw_stream(stream, dev)),
+    L.check(load().quip_adapter_plan(i, T, count, *_room("plan", plan, dev), _raw_stream(stream, dev)),
             "quip_adapter_plan")
     return plan
 
@@ -501,7 +509,7 @@ def quip_adapter_apply(x: torch.Tensor, ids: torch.Tensor, down: torch.Tensor, u
         px, _dtype(x), _row_stride(x), _here("ids", ids, _I32, (T,), dev), T, n, m, pd, pu, _dtype(down), count, r, ps,
         pb, 0 if base is None else _row_stride(base), py, _dtype(y), _row_stride(y),
         None if h is None else _here("h", h, _F32, (T, r), dev), _adapter_plan_ptr(plan, T, count, dev),
-        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _raw_stream(stream, dev)),
+        *((None, 0) if ws is None else _room("ws", ws, dev)), _raw_stream(stream, dev)),
         "quip_adapter_apply")
 
 
@@ -532,7 +540,7 @@ def quip_adapter_backward(x: torch.Tensor, dy: torch.Tensor, ids: torch.Tensor, 
         None if dx is None else _here("dx", dx, (x.dtype,), (T, n), dev, rows=True), 0 if dx is None else _row_stride(dx),
         None if d_down is None else _here("d_down", d_down, _F32, (count, r, n), dev),
         None if d_up is None else _here("d_up", d_up, _F32, (count, r, m), dev), int(accumulate),
-        _adapter_plan_ptr(plan, T, count, dev), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)),
+        _adapter_plan_ptr(plan, T, count, dev), *_room("ws", ws, dev), _raw_stream(stream, dev)),
         "quip_adapter_backward")
 
 

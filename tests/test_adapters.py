@@ -527,3 +527,40 @@ def test_quantized_layer_with_adapters_to_the_loss(clean):
     assert torch.equal(r2.logprob, lp)
     with pytest.raises(ValueError):
         hidden(x, adapters=ad)
+
+
+# ------------------------------------------------------------------ buffers that kernels write
+
+def test_buffers_on_the_host_are_refused():
+    from post_weight_quantization_09_b200 import _room
+    for name in ("plan", "ws"):
+        with pytest.raises(ValueError, match=f"{name} must be a CUDA tensor"):
+            _room(name, torch.empty(4096, dtype=torch.uint8), 0)
+
+
+@gpu
+def test_plans_and_workspaces_elsewhere_are_refused(clean):
+    c = Case(300, 64, 64, 32, 2)
+    nbytes = Q.quip_adapter_workspace_size(300, 64, 64, 32, 2, True)
+    plan = Q.quip_adapter_plan(c.ids, 2)
+    on_host = [torch.empty(nbytes, dtype=torch.uint8, pin_memory=p) for p in (False, True)]
+    gaps = torch.empty(2 * nbytes, dtype=torch.uint8, device="cuda")[::2]
+    c.y.fill_(7)
+    for bad in (*on_host, gaps):
+        with pytest.raises(ValueError, match="plan"):
+            Q.quip_adapter_plan(c.ids, 2, plan=bad)
+        with pytest.raises(ValueError, match="plan"):
+            c.apply(plan=bad[:plan.numel()])
+        with pytest.raises(ValueError, match="ws"):
+            c.apply(ws=bad)
+        with pytest.raises(ValueError, match="ws"):
+            c.backward(ws=bad)
+    assert torch.all(c.y == 7)
+    with pytest.raises(Q.QuipError):
+        c.apply(ws=gaps[:1])
+    # of any type, as long as the bytes are there
+    first = [t.clone() for t in (*c.apply(), *c.backward())]
+    ws = torch.empty(nbytes // 4, dtype=F, device="cuda")
+    assert all(torch.equal(a, b) for a, b in zip(first, (*c.apply(ws=ws), *c.backward(ws=ws))))
+    again = Q.quip_adapter_plan(c.ids, 2, plan=torch.empty(plan.numel() // 4, dtype=torch.int32, device="cuda"))
+    assert torch.equal(again[:6], plan.view(torch.int32)[:6])          # the header
