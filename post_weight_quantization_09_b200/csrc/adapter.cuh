@@ -685,10 +685,11 @@ inline ExpandRings expand_rings(int r16) {
   return e;
 }
 
-__device__ __forceinline__ void cp16(uint8_t* dst, const void* src, bool there) {   // 16 bytes, or zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
-               : "memory");
+// The first `bytes` of 16, zeros behind them.
+__device__ __forceinline__ void cp16(uint8_t* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp16(uint8_t* dst, const void* src, bool there) { cp16(dst, src, there ? 16 : 0); }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Eight consecutive values in registers.
@@ -1530,8 +1531,8 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
 #pragma unroll 8
             for (int k = 0; k < ROWS; k += AT_ONCE) {
               const int row = k + lane / CHS, t = __shfl_sync(0xffffffffu, mine, row);
-              const bool there = t >= 0 && left > 0;
-              cp16(xs + spot(row0 + row), a.x + (there ? (int64_t)t * a.ldx + c : 0), there);
+              const int bytes = t >= 0 ? min(16, max(0, 2 * left)) : 0;       // a row may end inside the 16
+              cp16(xs + spot(row0 + row), a.x + (bytes > 0 ? (int64_t)t * a.ldx + c : 0), bytes);
             }
             cp_wait_all();
           } else {

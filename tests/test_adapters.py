@@ -564,3 +564,28 @@ def test_plans_and_workspaces_elsewhere_are_refused(clean):
     assert all(torch.equal(a, b) for a, b in zip(first, (*c.apply(ws=ws), *c.backward(ws=ws))))
     again = Q.quip_adapter_plan(c.ids, 2, plan=torch.empty(plan.numel() // 4, dtype=torch.int32, device="cuda"))
     assert torch.equal(again[:6], plan.view(torch.int32)[:6])          # the header
+
+
+# ------------------------------------------------------------------ rows that end inside 16 bytes
+
+@gpu
+@pytest.mark.parametrize("x,y", [(B, B), (B, F), (F, B)])
+@pytest.mark.parametrize("T,n,m", [(1, 100, 36), (20, 100, 36), (70, 257, 999), (1500, 1, 7), (2500, 263, 134)])
+def test_widths_that_are_no_vectors_in_aligned_rows(clean, T, n, m, x, y):
+    # row strides that are multiples of 16 bytes, widths that are not: the
+    # buffers end with the last row's last value, and NaN lies between the rows
+    c = Case(T, n, m, 16, 2, x, B, y, "runs" if T > 1 else "one")
+    for name in ("x", "y", "base", "dy", "dx", "dx_base"):
+        t = getattr(c, name)
+        ld = (t.shape[1] + 15) // 8 * 8
+        buf = torch.full(((T - 1) * ld + t.shape[1],), float("nan"), dtype=t.dtype, device="cuda")
+        setattr(c, name, buf.as_strided(t.shape, (ld, 1)).copy_(t))
+        if name in ("y", "dx"):
+            setattr(c, name + "_buf", buf)
+    c.apply()
+    c.check_apply()
+    c.backward()
+    c.check_backward()
+    for buf, width in ((c.y_buf, m), (c.dx_buf, n)):
+        between = torch.arange(buf.numel(), device="cuda") % ((width + 15) // 8 * 8) >= width
+        assert torch.isnan(buf[between]).all() and not torch.isnan(buf[~between]).any()
