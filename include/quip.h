@@ -406,7 +406,10 @@ quip_status quip_qmatvec(const quip_transform* tf, const uint32_t* packed, int64
  *           Adapters of a smaller rank fill up with zero rows.
  *   scale : device count fp32, or NULL for 1.
  *   base  : device T x m of y's type, row stride ldb, or NULL for 0; may be y
- *           itself (ldb == ldy), else must not overlap it.
+ *           itself (ldb == ldy), else must not overlap it.  x and y must not overlap
+ *           either.  Column slices of one buffer (equal row strides in bytes)
+ *           do not; regions of other strides count with all between their first
+ *           and last byte.
  *   y     : device T x m, y_dtype QUIP_F32 or QUIP_BF16, row stride ldy.
  *   h     : device T x r fp32, or NULL: kept for quip_adapter_backward.
  *   plan  : from quip_adapter_plan for these ids, T and count (a model makes

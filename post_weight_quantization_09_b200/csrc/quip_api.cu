@@ -1888,11 +1888,19 @@ size_t type_bytes(int dtype) { return dtype == QUIP_BF16 ? 2 : 4; }
 bool rows_of_four(const void* p, int64_t ld, size_t size) {
   return (reinterpret_cast<uintptr_t>(p) % (4 * size)) == 0 && ld % 4 == 0;
 }
-// Whether two row-strided T x cols regions share a byte.
+// Whether two regions of T rows (strides in values) share a byte.  With equal
+// row strides exactly, so that column slices of one buffer do not; regions of
+// other strides by their spans.
 bool regions_overlap(const void* a, int64_t lda, int64_t cols_a, size_t size_a, const void* b, int64_t ldb,
                      int64_t cols_b, size_t size_b, int64_t T) {
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-  return pa < pb + ((T - 1) * ldb + cols_b) * size_b && pb < pa + ((T - 1) * lda + cols_a) * size_a;
+  const int64_t wa = cols_a * (int64_t)size_a, wb = cols_b * (int64_t)size_b;         // bytes of a row
+  const int64_t sa = lda * (int64_t)size_a, sb = ldb * (int64_t)size_b;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  if (sa != sb || T == 1) return d < (T - 1) * sa + wa && -d < (T - 1) * sb + wb;
+  // row i + q of a begins `in` bytes before row i of b, row i + q + 1 sa - in behind it
+  const int64_t q = d >= 0 ? d / sa : -((-d + sa - 1) / sa), in = d - q * sa;
+  auto rows_meet = [&](int64_t k) { return -T < k && k < T; };
+  return (rows_meet(q) && in < wa) || (rows_meet(q + 1) && sa - in < wb);
 }
 
 struct AdapterWs {
@@ -2350,13 +2358,9 @@ quip_status quip_logprobs_backward(const void* logits, int dtype, int64_t T, int
   if (ldd < V) return QUIP_ERR_SHAPE;
   if (T == 0) return QUIP_OK;
   if (!logits || !lse || !d_logits) return QUIP_ERR_ARG;
-  if (logits == d_logits) {
-    if (ld != ldd) return QUIP_ERR_ARG;
-  } else {
-    const uintptr_t e = dtype == QUIP_BF16 ? 2 : 4, a = reinterpret_cast<uintptr_t>(logits),
-                    b = reinterpret_cast<uintptr_t>(d_logits);
-    if (a < b + ((T - 1) * ldd + V) * e && b < a + ((T - 1) * ld + V) * e) return QUIP_ERR_ARG;
-  }
+  if (logits == d_logits ? ld != ldd
+                         : regions_overlap(logits, ld, V, type_bytes(dtype), d_logits, ldd, V, type_bytes(dtype), T))
+    return QUIP_ERR_ARG;
   cudaStream_t st = S(stream);
   QCHECK(dtype == QUIP_BF16
              ? logprobs_grad_launch<__nv_bfloat16>(logits, T, V, ld, tokens, lse, entropy, g_logprob, g_entropy,

@@ -589,3 +589,53 @@ def test_widths_that_are_no_vectors_in_aligned_rows(clean, T, n, m, x, y):
     for buf, width in ((c.y_buf, m), (c.dx_buf, n)):
         between = torch.arange(buf.numel(), device="cuda") % ((width + 15) // 8 * 8) >= width
         assert torch.isnan(buf[between]).all() and not torch.isnan(buf[~between]).any()
+
+
+def test_column_slices_of_one_buffer_are_accepted():
+    # Rows of 200 fp32 values hold x in columns [0, 64) and others beside it:
+    # no byte is shared.  Such a call gets as far as its workspace, which is too
+    # small here; one column less apart and it is refused.
+    lib = L.load()
+    at = lambda c: ctypes.c_void_p(0x1000000 + 4 * c)
+
+    def fw(y, base=None, ldx=200, ldy=200, T=1100):
+        return lib.quip_adapter_apply(at(0), 0, ldx, at(10 ** 8), T, 64, 32, at(2 * 10 ** 8), at(3 * 10 ** 8), 0, 2, 4, None,
+                                      base, 200, y, 0, ldy, None, None, None, 0, None)
+    for c in (64, 100, 168):
+        assert fw(at(c)) == L.QUIP_ERR_WORKSPACE, c
+    for c in (0, 1, 63, 169, 199):                                   # 169: the last column is the next row's first
+        assert fw(at(c)) == L.QUIP_ERR_ARG, c
+    assert fw(at(64 + 200 * 1099)) == L.QUIP_ERR_WORKSPACE           # beside x's last row, then past it
+    assert fw(at(63 + 200 * 1099)) == L.QUIP_ERR_ARG
+    assert fw(at(200 * 1100 - 1)) == fw(at(200 * 1100)) == L.QUIP_ERR_WORKSPACE
+    assert fw(at(-32 - 200 * 1099)) == fw(at(-32)) == L.QUIP_ERR_WORKSPACE
+    assert fw(at(-31)) == fw(at(-200 * 1099)) == L.QUIP_ERR_ARG
+    assert fw(at(64), base=at(96)) == L.QUIP_ERR_WORKSPACE           # x, y and base side by side
+    assert fw(at(64), base=at(95)) == fw(at(96), base=at(65)) == L.QUIP_ERR_ARG
+    assert fw(at(100), ldx=201) == L.QUIP_ERR_ARG                    # rows of other lengths: by their span
+
+    def bw(dx, b=None):
+        return lib.quip_adapter_backward(at(0), 0, 200, at(64), 0, 200, at(10 ** 8), 1100, 64, 32, at(2 * 10 ** 8),
+                                         at(3 * 10 ** 8), 0, 2, 4, None, None, b, 200, dx, 200, at(4 * 10 ** 8), None, 0,
+                                         None, None, 0, None)
+    assert bw(at(96)) == bw(at(136)) == bw(at(96), at(96)) == L.QUIP_ERR_WORKSPACE
+    assert bw(at(95)) == bw(at(137)) == bw(at(20)) == bw(at(96), at(97)) == L.QUIP_ERR_ARG
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("T", [7, 600])
+def test_column_slices_of_one_buffer(clean, T, dtype):
+    c = Case(T, 264, 136, 16, 3, dtype, B, dtype)
+    want = [t.clone() for t in (*c.apply(), *c.backward())]
+    buf = torch.full((T, 2 * 264 + 3 * 136 + 3), float("nan"), dtype=dtype, device="cuda")
+    at = 1
+    for name, width in (("x", 264), ("y", 136), ("base", 136), ("dy", 136), ("dx", 264)):
+        part = buf[:, at:at + width]
+        part.copy_(getattr(c, name))
+        setattr(c, name, part)
+        at += width
+    got = (*c.apply(), *c.backward())
+    assert all(torch.equal(a, b) for a, b in zip(want[2:], got[2:]))
+    c.check_apply()
+    assert torch.equal(want[0], got[0]) and torch.isnan(buf[:, 0]).all() and torch.isnan(buf[:, at:]).all()

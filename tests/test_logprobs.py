@@ -511,3 +511,18 @@ def test_gradient_with_the_sum_of_a_larger_vocabulary(clean):
     p = np.exp(x64 - lse64[:, None])
     tol = p * (8 + 3 * np.maximum(lse64[:, None] - x64, 0).clip(max=1000)) * U + 2 * U * np.abs(want) + 1e-37
     assert np.all(np.abs(host(d) - want) <= tol)
+
+
+@gpu
+def test_gradient_into_other_columns_of_the_logits_buffer(clean):
+    x, tokens = _logits(6, 1000, torch.float32, 4)
+    _, H, lse, _, _ = _run(x, tokens, 0)
+    g = torch.linspace(-1, 1, 6, device="cuda")
+    want, buf = torch.empty_like(x), torch.full((6, 2010), float("nan"), device="cuda")
+    Q.quip_logprobs_backward(x, tokens, lse, want, g_logprob=g, g_entropy=g, entropy=H)
+    buf[:, :1000] = x
+    Q.quip_logprobs_backward(buf[:, :1000], tokens, lse, buf[:, 1003:2003], g_logprob=g, g_entropy=g, entropy=H)
+    assert torch.equal(buf[:, 1003:2003], want) and torch.equal(buf[:, :1000], x)
+    assert torch.isnan(buf[:, 1000:1003]).all() and torch.isnan(buf[:, 2003:]).all()
+    with pytest.raises(Q.QuipError):
+        Q.quip_logprobs_backward(buf[:, :1000], tokens, lse, buf[:, 999:1999], g_logprob=g)
