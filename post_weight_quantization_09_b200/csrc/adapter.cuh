@@ -629,14 +629,15 @@ __global__ void __launch_bounds__(VT)
 // the products of pieces of order 2 and below are formed: fp32 operands keep
 // fp32 accuracy.  h is fed to the second product in pieces too: two for a
 // bf16 output (2^-17 is left, its rounding is 2^-9), three for an fp32 one.
-// The tensor core drops low bits of the running sum at every step, so the
-// blocks of n are dealt out over several accumulators that are added in fp32.
+// The tensor core drops low bits of the running sum at every step (of 16
+// products), so the 64-column blocks of n are dealt out over several
+// accumulators, 1024 columns to each at most, that are added in fp32
+// (ShrinkAccs).
 //
 // Loads are gathered by token into shared memory with the 128-byte swizzle,
 // by cp.async where bf16 rows allow 16-byte copies (CP), else through
 // registers, which also cuts fp32 values into pieces and takes any alignment.
 // Each stage has warps of its own that fill it, wait for it and hand it on.
-constexpr int TC_COLS = 256;                   // TMEM columns: two CTAs fit an SM (see shrink_smem)
 template <typename T> __host__ __device__ constexpr int pieces() { return sizeof(T) == 2 ? 1 : 3; }
 template <typename TY> __host__ __device__ constexpr int h_pieces() { return sizeof(TY) == 2 ? 2 : 3; }
 constexpr int XT_BYTES = TILE * 128;           // one piece of 128 tokens x 64 columns
@@ -659,8 +660,9 @@ __host__ __device__ inline int shrink_smem(int r16) {
   const int hp = TILE * (r16 + 4) * 4;         // the partial h, in the stages' place
   if (hp > s) s = hp;
   s += 1024;
-  // at most two CTAs on an SM: they hold 2 x 256 TMEM columns, so no CTA of
-  // a cluster ever waits for TMEM while its peers wait for it
+  // at most two CTAs on an SM, which hold 2 x 256 TMEM columns (bf16; with an
+  // fp32 operand the stages take 168 KB and more: one, with 512), so no CTA
+  // of a cluster ever waits for TMEM while its peers wait for it
   return s < 78 * 1024 ? 78 * 1024 : s;
 }
 // A block of the expand step is 256 bytes of y's rows; Q's tiles in flight and
@@ -745,18 +747,50 @@ template <> struct Eight<float> {
   }
 };
 
-// Accumulators of TC_COLS columns in all: the large terms' and, last, the one
-// that takes the small terms of operands in pieces.
-__host__ __device__ constexpr int tc_accs(int r16) { return r16 <= 64 ? 4 : 2; }
+// The accumulators of a CTA's `steps` blocks, r16 TMEM columns each: `mains`
+// take the large terms of the blocks in turn, `low` = 1 more, behind them, the
+// small terms of operands in pieces.  8 blocks (512 columns) meet in one where
+// TMEM has room, else up to 16; beyond, `round` blocks at a time (0: all at
+// once) are added up in fp32 and kept in the place behind these.  Sums of
+// 28672 positive fp32 terms in one CTA, rank 12, are off by 13 u on average (u
+// = 2^-24; by 600 u with all blocks in three accumulators).  The rounds' waits
+// cost 4096 bf16 tokens x 28672, rank 128, 83 us for 77.
+struct ShrinkAccs {
+  int mains, low, round;
+};
+template <bool SPLIT> __host__ __device__ constexpr int shrink_cols() { return SPLIT ? 512 : 256; }
+template <bool SPLIT>
+__host__ __device__ inline ShrinkAccs shrink_accs(int r16, int steps) {
+  const int low = SPLIT ? 1 : 0, most = shrink_cols<SPLIT>() / r16 - low, usual = (r16 <= 64 ? 4 : 2) - low;
+  if (steps > 16 * most) return {most - 1, low, 16 * (most - 1)};
+  const int want = (steps + 7) / 8;
+  return {want < usual ? usual : want < most ? want : most, low, 0};
+}
 
-template <typename TX, typename TW, bool CP>
+// The sum of accumulators 0 .. last into the columns from `to` on, the last
+// first; columns j0, j0 + step, ... by sixteen.
+__device__ __noinline__ void keep_round(uint32_t lanes, int j0, int step, int r16, int last, int to) {
+  for (int j = j0; j < r16; j += step) {
+    float v[16];
+    tmem_ld16(lanes + last * r16 + j, v);
+    for (int q = last - 1; q >= 0; --q) {
+      float w[16];
+      tmem_ld16(lanes + q * r16 + j, w);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] += w[e];
+    }
+    tmem_st16(lanes + to + j, v);
+  }
+}
+// acc: of the cluster's largest share of n; KEEP: with rounds.
+template <typename TX, typename TW, bool CP, bool KEEP>
 __global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
-    k_adapter_shrink(const __grid_constant__ ApplyArgs<TX, TW, float> a, void* plan) {
+    k_adapter_shrink(const __grid_constant__ ApplyArgs<TX, TW, float> a, const __grid_constant__ ShrinkAccs acc, void* plan) {
   constexpr int PX = pieces<TX>(), PW = pieces<TW>(), SW = stage_warps<CP>(), ST = stage_threads<CP>();
   constexpr bool SPLIT = PX > 1 || PW > 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int tok[TILE];
-  __shared__ uint64_t full[4], empty[4], all_done;
+  __shared__ uint64_t full[4], empty[4], all_done, round_done, round_kept;
   __shared__ uint32_t tmem_base;
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -775,12 +809,13 @@ __global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
   }
   const int r16 = (r + 15) / 16 * 16, stage = shrink_stage<TX, TW>(r16), stages = shrink_stages(stage);
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int blocks = (a.n + 63) / 64, per = (blocks + nc - 1) / nc;
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) mbar_init(&full[i], SW), mbar_init(&empty[i], 1);
-    mbar_init(&all_done, 1);
+    mbar_init(&all_done, 1), mbar_init(&round_done, 1), mbar_init(&round_kept, 4 * SW);
     fence_mbar_init();
   }
-  if (warp == 0) tmem_alloc(&tmem_base, TC_COLS);
+  if (warp == 0) tmem_alloc(&tmem_base, shrink_cols<SPLIT>());
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -788,9 +823,22 @@ __global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
   bool ok = true;                  // a wait that ran out is the last: what follows it is not stored
   const TW* P = a.P + (int64_t)l * r * a.n;
   // this CTA's 64-column blocks [k0, k0 + steps)
-  const int blocks = (a.n + 63) / 64, per = (blocks + nc - 1) / nc;
   const int k0 = min(blocks, rank * per), steps = min(blocks, k0 + per) - k0;
-  const int accs = tc_accs(r16), mains = SPLIT ? accs - 1 : accs;
+  int kept = 0;                    // rounds whose sum is kept
+  // the stages' warps, each once its blocks before `block` are there: keep the
+  // sums of the rounds before it
+  auto keep = [&](int block) {
+    for (; (kept + 1) * acc.round <= block; ++kept) {
+      ok = ok && mbar_wait(&round_done, (uint32_t)(kept & 1));
+      tc_fence_after();
+      if (32 * (warp % 4) < cnt)
+        keep_round(tmem + ((uint32_t)(32 * (warp % 4)) << 16), 16 * (warp / 4), 16 * SW, r16, acc.mains + acc.low - (kept > 0 ? 0 : 1),
+                   (acc.mains + acc.low) * r16);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&round_kept);
+    }
+  };
   if (warp < 4 * SW) {
     const int s = warp / SW;
     if (s < stages) {
@@ -799,7 +847,7 @@ __global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
       uint8_t* ps = xs + PX * XT_BYTES;
       auto spot = [&](int row) { return row * 128 + ((ch ^ (row & 7)) << 4); };
       // the lane's rows of x are those of every block
-      constexpr int ROWS = TILE / (4 * SW), BATCH = 4;
+      constexpr int ROWS = TILE / (4 * SW), BATCH = KEEP && SPLIT ? 2 : 4;
       int mine[ROWS];
 #pragma unroll
       for (int k = 0; k < ROWS; ++k) mine[k] = tok[row0 + 4 * SW * k];
@@ -853,21 +901,30 @@ __global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
+        if constexpr (KEEP) keep(i);
       }
     }
+    if constexpr (KEEP) keep(steps - 1);
   } else if (lane == 0) {
     // descriptors' addresses count 16 bytes: stages and steps are added to them
     const uint32_t idesc = make_idesc_bf16(TILE, r16, 0, 0);
     const uint64_t x0 = make_sw128_desc(smem_u32(sm), 16, 1024), p0 = x0 + (uint64_t)(PX * XT_BYTES >> 4);
     const int pp = r16 * 128 >> 4;
-    const uint32_t low = tmem + (uint32_t)((accs - 1) * r16);
-    for (int i = 0; i < steps && ok; ++i) {
-      const int s = i % stages;
-      ok = mbar_wait(&full[s], (uint32_t)((i / stages) & 1));
+    const uint32_t low = tmem + (uint32_t)(acc.mains * r16);
+    uint32_t large = tmem;                     // the block's accumulator
+    bool begun = false;                        // it holds blocks of this round
+    int s = 0, b = 0;                          // stage; the block's number in its round
+    uint32_t phase = 0;
+    for (int i = 0; i < steps && ok; ++i, ++b) {
+      if (KEEP && b == acc.round) {
+        b = 0, large = tmem, begun = false;
+        tc_commit(&round_done);
+        ok = mbar_wait(&round_kept, (uint32_t)((i / acc.round - 1) & 1));
+      }
+      ok = ok && mbar_wait(&full[s], phase);
       if (!ok) break;
       tc_fence_after();
       const uint64_t xd = x0 + (uint64_t)(s * stage >> 4), pd = p0 + (uint64_t)(s * stage >> 4);
-      const uint32_t large = tmem + (uint32_t)(i % mains * r16);
 #pragma unroll
       for (int px = 0; px < PX; ++px)
 #pragma unroll
@@ -876,9 +933,12 @@ __global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
           for (int kk = 0; kk < 4; ++kk) {
             const bool main = px + pw == 0, first = (PW > 1 ? px == 0 && pw == 1 : px == 1) && kk == 0;   // of the small terms
             tc_mma_f16(main ? large : low, xd + (uint64_t)((px * XT_BYTES >> 4) + kk * 2),
-                       pd + (uint64_t)(pw * pp + kk * 2), idesc, main ? (i >= mains || kk > 0) : (i > 0 || !first));
+                       pd + (uint64_t)(pw * pp + kk * 2), idesc, main ? (begun || kk > 0) : (b > 0 || !first));
           }
       tc_commit(&empty[s]);
+      if (++s == stages) s = 0, phase ^= 1u;
+      large += (uint32_t)r16;
+      if (large == low) large = tmem, begun = true;
     }
     if (steps > 0 && ok) tc_commit(&all_done);
   }
@@ -891,15 +951,16 @@ __global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
   float* hpart = reinterpret_cast<float*>(sm);
   if (warp < 4 && 32 * warp < cnt) {
     const int t = 32 * warp + lane;
-    const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16);
     for (int j = 0; j < r16; j += 16) {
       float v[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = 0.f;
-      for (int q = accs - 1; q >= 0; --q) {    // the small terms first
-        if (SPLIT && q == accs - 1 ? steps > 0 : q < steps) {
+      // from the rounds before and the small terms on; of the others those that were used
+      const int used = steps - kept * acc.round;
+      for (int q = acc.mains + acc.low - (KEEP && kept > 0 ? 0 : 1); q >= 0; --q) {
+        if (q >= acc.mains ? steps > 0 : q < used) {
           float w[16];
-          tmem_ld16(at + q * r16 + j, w);
+          tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + q * r16 + j, w);
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] += w[e];
         }
@@ -936,7 +997,7 @@ __global__ void __launch_bounds__(stage_threads<CP>(), CP ? 2 : 1)
   if (nc > 1) cluster.sync();                  // the others' shared memory is read until here
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, TC_COLS);
+    tmem_dealloc(tmem, shrink_cols<SPLIT>());
   }
 }
 
@@ -1528,11 +1589,12 @@ __global__ void __launch_bounds__(outer_threads<TX, CP>(), 1)
           }
           // rows past the adapter's tokens are 0: they would meet u's zeros as anything
           if constexpr (CP) {
+            const int bytes = min(16, 2 * left);         // the row may end inside the 16
 #pragma unroll 8
             for (int k = 0; k < ROWS; k += AT_ONCE) {
               const int row = k + lane / CHS, t = __shfl_sync(0xffffffffu, mine, row);
-              const int bytes = t >= 0 ? min(16, max(0, 2 * left)) : 0;       // a row may end inside the 16
-              cp16(xs + spot(row0 + row), a.x + (bytes > 0 ? (int64_t)t * a.ldx + c : 0), bytes);
+              const bool there = t >= 0 && left > 0;
+              cp16(xs + spot(row0 + row), a.x + (there ? (int64_t)t * a.ldx + c : 0), there ? bytes : 0);
             }
             cp_wait_all();
           } else {

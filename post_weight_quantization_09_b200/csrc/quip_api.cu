@@ -1970,21 +1970,33 @@ bool rows_of_eight(const void* p, int64_t ld, size_t size) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
 }
 
-template <bool CP, typename TX, typename TW>
-cudaError_t adapter_shrink(const ad::ApplyArgs<TX, TW, float>& a, void* plan, cudaStream_t st) {
+template <bool CP, bool KEEP, typename TX, typename TW>
+cudaError_t adapter_shrink_launch(const ad::ApplyArgs<TX, TW, float>& a, const ad::ShrinkAccs& acc, unsigned nc, int smem,
+                                  void* plan, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  auto* kernel = ad::k_adapter_shrink<TX, TW, CP>;
+  auto* kernel = ad::k_adapter_shrink<TX, TW, CP, KEEP>;
   cudaError_t e = allow_smem(kernel, 226 * 1024, done);
   if (e != cudaSuccess) return e;
-  // CTAs per cluster: as many as the SMs hold at once (one or two each) with a
-  // part-filled tile per adapter, each with a block at least
-  const int smem = ad::shrink_smem<TX, TW>((a.r + 15) / 16 * 16);
-  const int64_t resident = (CP && smem <= 112 * 1024 ? 2 : 1) * (int64_t)num_sms();
-  const int64_t likely = (a.T + ad::TILE - 1) / ad::TILE + std::min<int64_t>(a.count, a.T / 16), blocks = (a.n + 63) / 64;
-  const unsigned nc = (unsigned)std::min<int64_t>(std::min<int64_t>(8, blocks), std::max<int64_t>(1, resident / likely));
   LaunchScope ls("k_adapter_shrink", st);
   return launch_cluster(kernel, (unsigned)(ad::max_tiles(a.T, a.count, ad::TILE) * nc), ad::stage_threads<CP>(),
-                        smem, nc, true, st, a, plan);
+                        smem, nc, true, st, a, acc, plan);
+}
+template <bool CP, typename TX, typename TW>
+cudaError_t adapter_shrink(const ad::ApplyArgs<TX, TW, float>& a, void* plan, cudaStream_t st) {
+  // CTAs per cluster: as many as the SMs hold at once (one or two each) with a
+  // part-filled tile per adapter, each with a block at least
+  const int r16 = (a.r + 15) / 16 * 16, smem = ad::shrink_smem<TX, TW>(r16);
+  const int64_t resident = (CP && smem <= 112 * 1024 ? 2 : 1) * (int64_t)num_sms();
+  const int64_t likely = (a.T + ad::TILE - 1) / ad::TILE + std::min<int64_t>(a.count, a.T / 16), blocks = (a.n + 63) / 64;
+  unsigned nc = (unsigned)std::min<int64_t>(std::min<int64_t>(8, blocks), std::max<int64_t>(1, resident / likely));
+  constexpr bool split = ad::pieces<TX>() > 1 || ad::pieces<TW>() > 1;
+  auto accs = [&] { return ad::shrink_accs<split>(r16, (int)((blocks + nc - 1) / nc)); };
+  // with an fp32 operand more CTAs rather than rounds, which cost it more:
+  // 2400 tokens x 8192, rank 64, 299 us with one CTA a tile in rounds, 124 with two
+  while (split && nc <= 4 && accs().round) nc *= 2;
+  const ad::ShrinkAccs acc = accs();
+  return acc.round ? adapter_shrink_launch<CP, true>(a, acc, nc, smem, plan, st)
+                   : adapter_shrink_launch<CP, false>(a, acc, nc, smem, plan, st);
 }
 
 template <bool CP, typename TW, typename TY>

@@ -639,3 +639,29 @@ def test_column_slices_of_one_buffer(clean, T, dtype):
     assert all(torch.equal(a, b) for a, b in zip(want[2:], got[2:]))
     c.check_apply()
     assert torch.equal(want[0], got[0]) and torch.isnan(buf[:, 0]).all() and torch.isnan(buf[:, at:]).all()
+
+
+# ------------------------------------------------------------------ long rows
+
+@gpu
+@pytest.mark.parametrize("x,w,r,n,count", [
+    (F, F, 12, 28672, 1), (F, F, 12, 28672, 1024), (F, F, 64, 9000, 1024), (F, F, 64, 70000, 1), (F, B, 128, 11008, 1),
+    (F, B, 128, 11008, 1024), (F, B, 128, 28700, 1), (F, B, 100, 5003, 1024), (B, B, 16, 28672, 1), (B, B, 16, 28672, 1024),
+    (B, B, 33, 20000, 1024), (B, B, 96, 28672, 1), (B, B, 128, 2112, 1024), (B, B, 128, 11008, 1024), (B, B, 128, 11007, 1024)])
+def test_long_sums_of_one_sign(clean, x, w, r, n, count):
+    # Sums whose every term is positive lose what the tensor core drops at each
+    # step in one direction.  A step adds 16 products and may drop 2 u of the
+    # running sum; at most 1024 columns (64 steps) meet in an accumulator, then
+    # fp32 sums of n / 512 + 8 parts, however many adapters are loaded.
+    T, m = 2400, 8
+    g = torch.Generator().manual_seed(n)
+    xs = (torch.rand(T, n, generator=g) + 0.5).to(x).cuda()
+    down = torch.zeros(count, r, n, dtype=w, device="cuda")
+    down[-1] = (torch.rand(r, n, generator=g) + 0.5).to(w).cuda()
+    up = torch.zeros(count, r, m, dtype=w, device="cuda")
+    ids = torch.full((T,), count - 1, dtype=torch.int32, device="cuda")
+    y, h = torch.empty(T, m, dtype=x, device="cuda"), torch.empty(T, r, device="cuda")
+    Q.quip_adapter_apply(xs, ids, down, up, None, y, h=h)
+    want = xs.double() @ down[-1].double().T
+    off = ((h.double() - want).abs() / want).max().item()
+    assert off <= (128 + 8 + n / 512) * U, off / U
