@@ -397,6 +397,8 @@ class QuantizedLinear:
             raise ValueError(f"batch {x.shape[0]} > max_batch {self.max_batch}")
         if (adapters is None) != (ids is None):
             raise ValueError("adapters and ids go together")
+        if adapters is None and (h is not None or plan is not None):
+            raise ValueError("h and plan belong to adapters")
         if out is None:
             out = torch.empty(x.shape[0], self.m, dtype=torch.float32, device=x.device)
         quip_qmatvec(self.tf, self.packed, self.lo, self.scale, self.bits, x, out, self.ws, self.stream)

@@ -665,3 +665,14 @@ def test_long_sums_of_one_sign(clean, x, w, r, n, count):
     want = xs.double() @ down[-1].double().T
     off = ((h.double() - want).abs() / want).max().item()
     assert off <= (128 + 8 + n / 512) * U, off / U
+
+
+# ------------------------------------------------------------------ arguments without their adapters
+
+def test_layer_refuses_what_only_adapters_take():
+    layer = object.__new__(Q.QuantizedLinear)
+    layer.max_batch = 8
+    x = torch.zeros(2, 8)
+    for extra in (dict(h=torch.zeros(2, 4)), dict(plan=torch.zeros(256, dtype=torch.uint8)), dict(ids=torch.zeros(2))):
+        with pytest.raises(ValueError, match="adapters"):
+            layer(x, **extra)
