@@ -311,18 +311,24 @@ constexpr int VT = 256;                        // threads per CTA
 constexpr int EARLY = 16;                      // rows of Q asked for at once
 constexpr int TOKEN_CTAS = 8;                  // of a cluster, at most
 
-// Four consecutive values as they lie in memory.
+// Four consecutive values as they lie in memory.  CONST: nothing writes them
+// while the kernel runs (base may be y itself).
 template <typename T> struct Four;
 template <> struct Four<float> {
   float4 v;
-  __device__ __forceinline__ void load(const float* p, bool vec, int left) { v = load4(p, vec, left); }
+  template <bool CONST = true>
+  __device__ __forceinline__ void load(const float* p, bool vec, int left) {
+    if (!CONST && vec && left >= 4) v = *reinterpret_cast<const float4*>(p);
+    else v = load4(p, vec, left);
+  }
   __device__ __forceinline__ float4 get() const { return v; }
 };
 template <> struct Four<__nv_bfloat16> {
   uint2 v;
+  template <bool CONST = true>
   __device__ __forceinline__ void load(const __nv_bfloat16* p, bool vec, int left) {
     if (vec && left >= 4) {
-      v = __ldg(reinterpret_cast<const uint2*>(p));
+      v = CONST ? __ldg(reinterpret_cast<const uint2*>(p)) : *reinterpret_cast<const uint2*>(p);
     } else {
       auto at = [&](int i) { return i < left ? (uint32_t)__bfloat16_as_ushort(p[i]) : 0u; };
       v = make_uint2(at(0) | at(1) << 16, at(2) | at(3) << 16);
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(VT, sizeof(TW) == 2 ? 4 : 2)
   if (y && c0 < m1) {
 #pragma unroll
     for (int j = 0; j < EARLY; ++j) early[j].load(Q + (int64_t)min(j, r - 1) * a.m + c0, a.vec_q, m1 - c0);
-    if (base) early_base.load(base + c0, a.vec_y, m1 - c0);
+    if (base) early_base.template load<false>(base + c0, a.vec_y, m1 - c0);
   }
   cluster.barrier_wait(std::move(running));
   for (int j0 = R * warp; j0 < r; j0 += R * (VT / 32)) {
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(VT, sizeof(TW) == 2 ? 4 : 2)
     if (c != c0) {
 #pragma unroll
       for (int j = 0; j < EARLY; ++j) early[j].load(Q + (int64_t)min(j, r - 1) * a.m + c, a.vec_q, m1 - c);
-      if (base) early_base.load(base + c, a.vec_y, m1 - c);
+      if (base) early_base.template load<false>(base + c, a.vec_y, m1 - c);
     }
 #pragma unroll
     for (int j = 0; j < EARLY; ++j)

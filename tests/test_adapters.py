@@ -676,3 +676,16 @@ def test_layer_refuses_what_only_adapters_take():
     for extra in (dict(h=torch.zeros(2, 4)), dict(plan=torch.zeros(256, dtype=torch.uint8)), dict(ids=torch.zeros(2))):
         with pytest.raises(ValueError, match="adapters"):
             layer(x, **extra)
+
+
+@gpu
+@pytest.mark.parametrize("x,w,y", TYPES)
+@pytest.mark.parametrize("T,m,pad", [(1, 11008, 0), (16, 4100, 4), (64, 9001, 1)])
+def test_few_tokens_in_place(clean, T, m, pad, x, w, y):
+    # base is y itself, several rounds of columns per thread
+    c = Case(T, 96, m, 16, 3, x, w, y, pad=pad)
+    want = c.apply()[0].clone()
+    c.y.copy_(c.base)
+    Q.quip_adapter_apply(c.x, c.ids, c.down, c.up, c.scale, c.y, base=c.y, h=c.h)
+    assert torch.equal(c.y, want)
+    c.check_apply()
