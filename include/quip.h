@@ -406,10 +406,10 @@ quip_status quip_qmatvec(const quip_transform* tf, const uint32_t* packed, int64
  *           Adapters of a smaller rank fill up with zero rows.
  *   scale : device count fp32, or NULL for 1.
  *   base  : device T x m of y's type, row stride ldb, or NULL for 0; may be y
- *           itself (ldb == ldy), else must not overlap it.  x and y must not overlap
- *           either.  Column slices of one buffer (equal row strides in bytes)
- *           do not; regions of other strides count with all between their first
- *           and last byte.
+ *           itself (ldb == ldy), else must not overlap it; nor may x and y
+ *           overlap.  Column slices of one buffer (equal row strides in bytes)
+ *           do not; a region beside one of another stride counts with all
+ *           between its first and last byte.
  *   y     : device T x m, y_dtype QUIP_F32 or QUIP_BF16, row stride ldy.
  *   h     : device T x r fp32, or NULL: kept for quip_adapter_backward.
  *   plan  : from quip_adapter_plan for these ids, T and count (a model makes
@@ -420,10 +420,11 @@ quip_status quip_qmatvec(const quip_transform* tf, const uint32_t* packed, int64
  *   ws    : quip_adapter_workspace_size(..., 0) bytes, none (NULL) where that
  *           is 0 (small batches) or where both a plan and h are given.
  * Sums are fp32; y is rounded once.  A token whose x, h or product is not
- * finite gets NaN or infinities in its own rows, no other token does.  1 <= r <= QUIP_ADAPTER_MAX_RANK,
- * 1 <= count <= QUIP_ADAPTER_MAX_COUNT, T <= 2^22, n, m <= 2^24; T = 0 does
- * nothing.  Any alignment and strides; 16-byte aligned rows of bf16 are
- * fastest.
+ * finite (or an fp32 value that rounds to infinity in bf16, from 3.396e38 on)
+ * gets NaN or infinities in its own rows, no other token does.
+ * 1 <= r <= QUIP_ADAPTER_MAX_RANK, 1 <= count <= QUIP_ADAPTER_MAX_COUNT,
+ * T <= 2^22, n, m <= 2^24; T = 0 does nothing.  Any alignment and strides;
+ * 16-byte aligned rows of bf16 are fastest.
  */
 quip_status quip_adapter_apply(const void* x, int x_dtype, int64_t ldx, const int32_t* ids, int64_t T, int64_t n,
                                int64_t m, const void* down, const void* up, int w_dtype, int64_t count, int64_t r,
@@ -487,8 +488,11 @@ quip_status quip_adapter_workspace_size(int64_t T, int64_t n, int64_t m, int64_t
  *   logprob, entropy, lse : device T fp32; entropy and lse may be NULL.
  *   k      : 0 .. min(V, QUIP_LOGPROBS_MAX_TOP); top_values (fp32) and top_ids
  *            (int32): device T x k, ignored when k is 0.
- * A logit of -inf has probability 0.  A row of nothing else has lse,
- * logprob and top_values -inf and entropy 0.  A NaN or +inf makes the row's
+ * A logit of -inf has probability 0, as has any finite one far enough below
+ * the row's largest (masks).  A row of -inf only has lse, logprob and
+ * top_values -inf and entropy 0.  Such rows, and rows whose largest logit is
+ * 2839 or more in size, are summed by one warp: 4096 x 32000 bf16 logits around
+ * 5000 take 480 us, others 51.  A NaN or +inf makes the row's
  * values NaN (its top_ids are then unspecified, in [0, V)).
  * T <= 2^22, V <= 2^28; T = 0 does nothing.
  */

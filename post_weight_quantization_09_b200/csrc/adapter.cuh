@@ -9,8 +9,9 @@
 // are one kernel for an outer product summed over an adapter's tokens.
 //
 // Forward and gradient of the activations take 2 T r (n + m) flops each, the
-// weight gradients as much; at ranks up to 64 the bytes of x, y and dy bound
-// all of them (rank 64 does 64 flops a byte, the GPU 250).
+// weight gradients as much; at ranks up to 64 the bytes of x, y and dy are the
+// floor of all of them (rank 64 does 64 flops a byte, the GPU 250).  What
+// bounds each kernel as built stands there.
 //
 // By the number of tokens (adapter_direct in quip_api.cu): few go straight
 // from ids, a cluster per token; more are grouped by adapter first (the plan)
@@ -44,7 +45,7 @@ constexpr int MAX_RANK = QUIP_ADAPTER_MAX_RANK;
 //           sums; sub: the number of its first SUB tokens among all runs of SUB
 //   parts   (first slot, number of slots) per adapter, 0 slots with one chunk
 constexpr int HEAD = 16, TILE = 128, SMALL = 8, CHUNK = 1024, SUB = 64;
-enum { H_MAGIC, H_T, H_COUNT, H_TILES, H_SMALL, H_CHUNKS, H_BAD };
+enum { H_MAGIC, H_T, H_COUNT, H_TILES, H_SMALL, H_CHUNKS };
 constexpr int MAGIC = 0x51AD;
 
 struct PlanView {
@@ -628,8 +629,7 @@ __global__ void __launch_bounds__(VT)
 // each lane on its own row's bytes).  By clocks read in the kernel the
 // multiplying warp bounds it: of 2450 clocks a block it spends 1180 on its
 // eight products, 620 on the fence and the commit around them, 290 waiting;
-// a group of row warps needs a block's rows for 5100 of 4 x 2450.  16 tokens
-// to a tile and fp32 rows: 1100 of 1900, before the products were one loop.
+// a group of row warps needs a block's rows for 5100 of 4 x 2450.
 //
 // Types: a bf16 value is one operand piece, an fp32 value three (split3), and
 // the products of pieces of order 2 and below are formed: fp32 operands keep

@@ -1937,7 +1937,9 @@ cudaError_t adapter_plan(const int32_t* ids, int64_t T, int64_t count, void* pla
 // Whether a cluster per token, without a plan, is taken: it reads a token's
 // adapter from L2 for every token, the tiles pay for the plan and their start.
 // 4096 -> 11008, rank 16, 32 adapters: 27 and 57 us for 128 tokens, 47 and 71
-// for 256, 84 and 75 for 512; rank 64: 149 and 69 us for 128.
+// for 256, 84 and 75 for 512; rank 64: 149 and 69 us for 128.  With few adapters
+// the tiles are fuller (512 tokens over four: 37 us) and win earlier; the rule
+// does not look at that.
 bool adapter_direct(int64_t T, int64_t r) { return T <= 16 || T * r <= 4096; }
 
 // CTAs per cluster of up to 8: as the SMs are filled and each still has some
@@ -2303,8 +2305,8 @@ quip_status quip_adapter_backward(const void* x, int x_dtype, int64_t ldx, const
 
 // ------------------------------------------------------------------ log probabilities
 namespace {
-// CTAs per row: more where the rows leave SMs idle (k_logprobs keeps four
-// CTAs on an SM) and each still gets a few thousand logits.
+// CTAs per row: more where the rows leave SMs idle (up to four CTAs on each;
+// five fit) and each still gets a few thousand logits.
 unsigned logprobs_cluster(int64_t T, int64_t V) {
   unsigned nc = 1;
   while (nc < lp::MAX_CLUSTER && T * nc * 2 <= 4 * (int64_t)num_sms() && V / (nc * 2) >= 2048) nc *= 2;
