@@ -11,12 +11,12 @@
 //
 //   k_ldl_factor(p)  R_pp = backward Cholesky of the updated diagonal block,
 //                    with the inverses X_J of its four 32 x 32 diagonal
-//                    blocks, the block's Ů and D, and the 128 "next" rows
+//                    blocks, D, and the 128 "next" rows
 //                    Nx = R12(p)[c0-128 : c0] (4 CTAs, each factors the block
 //                    redundantly and solves 32 of those rows);
 //   k_ldl_rows(p)    R12(p) = H[:c0, panel p] R_pp^-T (32 rows per block;
-//                    the rows of Nx are taken from there), its Ů and bf16
-//                    pieces, and the look-ahead product L(p) = R12(p) Nx^T,
+//                    the rows of Nx are taken from there), its and the
+//                    diagonal block's Ů, R12's bf16 pieces, and the look-ahead product L(p) = R12(p) Nx^T,
 //                    i.e. panel p's update of panel p - 1, into a side buffer;
 //   bulk(p)          H[:c0-128, :c0-128] -= R12 R12^T (upper tiles; tensor-
 //                    core split GEMM on a second stream, quip_api.cu).
@@ -328,8 +328,9 @@ __device__ __forceinline__ float* align128(uint8_t* p) {
 // CTA c (when c0 > 0) solves next rows c0 - 128 + 32 c .. + 31 of R12(p)
 // into Nx (128 x 128, row i = global row c0 - 128 + i).  The CTAs split the
 // stores of R_pp (Rd, 128 x 128, upper; lower zero) and X_J (Xw, 4 x 32 x
-// 32); CTA 0 writes D (Dv[c0 + k] = R_kk^2); the CTAs split the block's rows
-// for its Ů in H.  Lin: the look-ahead buffer of panel p + 1 (rows
+// 32); CTA 0 writes D (Dv[c0 + k] = R_kk^2).  The block's Ů goes to H only in
+// k_ldl_rows (here for c0 = 0, where there is one CTA): a CTA that starts late
+// still reads the block from H when another is done.  Lin: the look-ahead buffer of panel p + 1 (rows
 // [0, c0 + 128) x 128), or NULL.
 // Dynamic smem: (128 + 32) x LDL_LDA + 5 x 32 x LDL_LDX + 96 floats.
 __global__ void __launch_bounds__(LDL_FT, 1)
@@ -428,15 +429,12 @@ __global__ void __launch_bounds__(LDL_FT, 1)
         Dv[c0 + k] = r * r;
       }
   }
-  {
-    // this CTA's share of the block's Ů
-    const int rows = LDL_PB / gridDim.x, i0 = rows * blockIdx.x;
-    for (int e = tid; e < rows * LDL_PB; e += LDL_FT) {
-      const int i = i0 + (e >> 7), j = e & 127;
+  if (!has_next) {
+    for (int e = tid; e < LDL_PB * LDL_PB; e += LDL_FT) {
+      const int i = e >> 7, j = e & 127;
       if (i < j && j < w) H[(c0 + i) * n + c0 + j] = A[i * LDL_LDA + j] / A[j * LDL_LDA + j];
     }
-  }
-  if (has_next) {
+  } else {
     for (int e = tid; e < 32 * 32; e += LDL_FT) {
       const int i = e >> 5, j4 = (e & 31) * 4;
       *reinterpret_cast<float4*>(Nx + (32 * blockIdx.x + i) * LDL_PB + j4) =
@@ -453,7 +451,8 @@ __global__ void __launch_bounds__(LDL_FT, 1)
 // gridDim.x, ... < nblk) of panel p:
 //   R12 = (H - Lin)[rows, panel p] R_pp^-T by block back substitution with
 //         R_pp (Rd) and X_J (Xw); rows in [c0 - 128, c0) are taken from Nx;
-//   Ů:    H[r, c0 + k] = R12[r][k] / R_kk          (k < w)
+//   Ů:    H[r, c0 + k] = R12[r][k] / R_kk          (k < w); CTA b < 4 also writes
+//         rows c0 + 32 b .. + 31 of the diagonal block's, from R_pp
 //   Rs:   R12 as three bf16 pieces Rs[q][r][k]     (piece stride n * 128; zero for k >= w)
 //   Lout[r][j] = sum_k R12[r][k] Nx[j][k]          (panel p's update of panel p - 1)
 // 256 threads; Lout's product: warp v columns [16 v, 16 v + 16), lane
@@ -552,6 +551,13 @@ __global__ void __launch_bounds__(LDL_RT, 1)
       for (int q = 0; q < 3; ++q)
         *reinterpret_cast<uint2*>(Rs + q * pstride + g * LDL_PB + k4) =
             *reinterpret_cast<const uint2*>(pc[q]);
+    }
+
+    if (it == 0 && blockIdx.x < 4) {              // nblk >= 4: c0 >= 128
+      for (int e = tid; e < 32 * LDL_PB; e += LDL_RT) {
+        const int i = 32 * blockIdx.x + (e >> 7), j = e & 127;
+        if (i < j && j < w) H[(c0 + i) * n + c0 + j] = Rp[i * LDL_LDA + j] / rkk[j];
+      }
     }
 
     // Lout = R12 Nx^T, staged in Lt for row-contiguous stores

@@ -548,3 +548,28 @@ def test_timing_trace_lists_the_layer_launches():
     agg = Q.quip_timing_end()
     assert sum(c for c, _ in agg.values()) == len(tr)
     assert agg["k_syrk_tc"][0] == names.count("k_syrk_tc")
+
+
+def test_ldl_beside_other_work():
+    # The CTAs that share a panel's diagonal block may start far apart when
+    # other work fills the SMs: the factor stays the same to the bit.
+    n = 2048
+    rng = np.random.default_rng(8)
+    G = rng.standard_normal((n, 64))
+    H = dev(np.eye(n) * 0.5 + G @ G.T / 64)
+    want, D, D0 = H.clone(), torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    Q.quip_ldl(want, D0)
+    a = torch.randn(2048, 2048, device="cuda")
+    busy = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(25):
+        for s in busy:
+            with torch.cuda.stream(s):
+                for _ in range(4):
+                    torch.mm(a, a)
+                    torch.sin(a)
+        got = H.clone()
+        Q.quip_ldl(got, D)
+        torch.cuda.synchronize()
+        assert Q.quip_sync_status() == L.QUIP_OK
+        assert torch.equal(got.triu(), want.triu()) and torch.equal(D, D0)
